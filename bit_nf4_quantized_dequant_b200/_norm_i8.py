@@ -1,0 +1,270 @@
+"""ctypes binding of ``include/qlora_i8.h``: the RMS norm and the 8-bit integer
+linear. As in ``_binding``, every function maps onto one C entry point and
+allocates what the caller does not pass; no step of the computation runs here.
+
+Shapes, types, devices and contiguity are checked here, since the C side only
+sees pointers: a tensor that does not fit raises ``ValueError`` before the call.
+"""
+
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+
+import torch
+
+from . import _binding
+
+__all__ = [
+    "I8Matrix", "SYMBOLS_I8", "i8_quantize", "i8_dequantize", "rmsnorm_fwd", "rmsnorm_bwd", "rmsnorm_workspace",
+    "i8_linear_fwd", "i8_linear_dx", "i8_linear_workspace",
+]
+
+# every symbol include/qlora_i8.h declares
+SYMBOLS_I8 = [
+    "qlora_i8_quantize", "qlora_i8_dequantize", "qlora_rmsnorm_fwd", "qlora_rmsnorm_workspace", "qlora_rmsnorm_bwd",
+    "qlora_i8_linear_fwd", "qlora_i8_linear_workspace", "qlora_i8_linear_dx",
+]
+
+_BF16, _F32, _I8 = torch.bfloat16, torch.float32, torch.int8
+_TYPE = {_BF16: 0, _F32: 1}
+_lib = None
+
+
+def _library():
+    global _lib
+    if _lib is None:
+        lib = _binding.library()
+        P, I32, I64, F, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float, ctypes.c_size_t
+        PSZ = ctypes.POINTER(SZ)
+        for name, args in (
+                ("qlora_i8_quantize", [P, I32, I64, I64, P, P, P, P]),
+                ("qlora_i8_dequantize", [P, P, I64, I64, P, P]),
+                ("qlora_rmsnorm_fwd", [P, P, I32, P, I32, F, I64, I64, P, P, P, P, P]),
+                ("qlora_rmsnorm_workspace", [I64, I64, PSZ]),
+                ("qlora_rmsnorm_bwd", [P, P, I32, P, I32, F, P, I64, I64, P, P, P, P, SZ, P]),
+                ("qlora_i8_linear_fwd", [P, P, I64, P, P, I64, I64, P, P, I32, P, P, P]),
+                ("qlora_i8_linear_workspace", [I64, I64, I64, PSZ]),
+                ("qlora_i8_linear_dx", [P, I64, P, P, I64, I64, P, P, I32, P, P, SZ, P, P])):
+            fn = getattr(lib, name)
+            fn.argtypes, fn.restype = args, ctypes.c_int
+        _lib = lib
+    return _lib
+
+
+def _need(t, name, dtypes, shape, device):
+    """A contiguous CUDA tensor of one of these types and this shape, on `device`: its address."""
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous")
+    return t.data_ptr()
+
+
+def _opt(t, name, dtypes, shape, device):
+    return None if t is None else _need(t, name, dtypes, shape, device)
+
+
+def _device(t, name):
+    """The device of a call: that of its first tensor, which has to be the current one."""
+    d = t.device
+    if d.type != "cuda":
+        raise ValueError(f"{name}: on {d}, expected a CUDA device")
+    if d.index != torch.cuda.current_device():
+        raise ValueError(f"{name}: on {d}, but the current device is cuda:{torch.cuda.current_device()}")
+    return d
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError(f"{name}: {t.dim()} dimensions, expected a matrix")
+    return t.shape
+
+
+class _Call:
+    """The stream of a call, and the tensors allocated for it: memory comes from
+    the current stream's pool, so another stream's use of it is recorded."""
+
+    __slots__ = ("other", "handle", "device")
+
+    def __init__(self, stream, device):
+        current = torch.cuda.current_stream()
+        self.other = stream if stream is not None and stream != current else None
+        self.handle = (self.other or current).cuda_stream
+        self.device = device
+
+    def empty(self, shape, dtype):
+        t = torch.empty(shape, dtype=dtype, device=self.device)
+        if self.other is not None:
+            self.other.wait_stream(torch.cuda.current_stream())   # the memory may still be in use there
+            t.record_stream(self.other)
+        return t
+
+
+_check = _binding._check
+
+
+@dataclass
+class I8Matrix:
+    """Int8 rows: codes int8 [rows, cols] and one fp32 scale a row [rows]."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+
+    @classmethod
+    def empty(cls, rows: int, cols: int, device="cuda"):
+        return cls(torch.empty((rows, cols), dtype=_I8, device=device),
+                   torch.empty(rows, dtype=_F32, device=device))
+
+
+def _need_i8(q, name, shape, device):
+    return (_need(q.codes, name + ".codes", (_I8,), shape, device),
+            _need(q.scale, name + ".scale", (_F32,), (shape[0],), device))
+
+
+def i8_quantize(X, col_scale=None, out: I8Matrix | None = None, stream=None) -> I8Matrix:
+    """Int8 rows of X [M, K] (bf16 or fp32), or of X * col_scale[K]."""
+    M, K = shape = _matrix(X, "X")
+    dev = _device(X, "X")
+    call = _Call(stream, dev)
+    x = _need(X, "X", (_BF16, _F32), shape, dev)
+    if out is None:
+        out = I8Matrix(call.empty(shape, _I8), call.empty((M,), _F32))
+    codes, scale = _need_i8(out, "out", shape, dev)
+    _check(_library().qlora_i8_quantize(x, _TYPE[X.dtype], M, K, _opt(col_scale, "col_scale", (_F32,), (K,), dev),
+                                        codes, scale, call.handle), "qlora_i8_quantize")
+    return out
+
+
+def i8_dequantize(q: I8Matrix, out=None, stream=None):
+    """codes * scale as bf16 [M, K]."""
+    M, K = shape = _matrix(q.codes, "codes")
+    dev = _device(q.codes, "codes")
+    call = _Call(stream, dev)
+    codes, scale = _need_i8(q, "q", shape, dev)
+    if out is None:
+        out = call.empty(shape, _BF16)
+    _check(_library().qlora_i8_dequantize(codes, scale, M, K, _need(out, "out", (_BF16,), shape, dev), call.handle),
+           "qlora_i8_dequantize")
+    return out
+
+
+def rmsnorm_fwd(X, weight, eps: float, residual=None, H=None, Y=None, q: I8Matrix | None = None,
+                want_H: bool = True, stream=None):
+    """RMS norm of h = X + residual (either may be None). Returns (Y, H, q): the
+    outputs that are passed are written; Y (bf16) is allocated when neither Y nor
+    q (int8 rows) is passed, H (the stream's type) when both X and residual are
+    given and want_H."""
+    first = residual if residual is not None else X
+    if first is None:
+        raise ValueError("X or residual is needed")
+    M, K = shape = _matrix(first, "residual" if residual is not None else "X")
+    dev = _device(first, "residual" if residual is not None else "X")
+    call = _Call(stream, dev)
+    ht = _BF16 if residual is None else residual.dtype
+    x = _opt(X, "X", (_BF16,), shape, dev)
+    r = _opt(residual, "residual", (_BF16, _F32), shape, dev)
+    w = _need(weight, "weight", (_BF16, _F32), (K,), dev)
+    if Y is None and q is None:
+        Y = call.empty(shape, _BF16)
+    if H is None and want_H and X is not None and residual is not None:
+        H = call.empty(shape, ht)
+    codes, scale = (None, None) if q is None else _need_i8(q, "q", shape, dev)
+    _check(_library().qlora_rmsnorm_fwd(x, r, _TYPE[ht], w, _TYPE[weight.dtype], eps, M, K,
+                                        _opt(H, "H", (ht,), shape, dev), _opt(Y, "Y", (_BF16,), shape, dev),
+                                        codes, scale, call.handle), "qlora_rmsnorm_fwd")
+    return Y, H, q
+
+
+def rmsnorm_workspace(M: int, K: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_library().qlora_rmsnorm_workspace(M, K, ctypes.byref(b)), "qlora_rmsnorm_workspace")
+    return b.value
+
+
+def rmsnorm_bwd(dY, H, weight, eps: float, dres=None, dH=None, dX=None, dW=None, ws=None, want_dW: bool = True,
+                stream=None):
+    """(dH, dX, dW): the gradient of the stream h in its type, its bf16 copy
+    (only when dX is passed) and the weight's (fp32, or None without want_dW)."""
+    M, K = shape = _matrix(dY, "dY")
+    dev = _device(dY, "dY")
+    call = _Call(stream, dev)
+    ht = H.dtype
+    dy = _need(dY, "dY", (_BF16,), shape, dev)
+    h = _need(H, "H", (_BF16, _F32), shape, dev)
+    w = _need(weight, "weight", (_BF16, _F32), (K,), dev)
+    dr = _opt(dres, "dres", (ht,), shape, dev)
+    if dH is None:
+        dH = call.empty(shape, ht)
+    if dW is None and want_dW:
+        dW = call.empty((K,), _F32)
+    if dW is not None and ws is None:
+        ws = call.empty((rmsnorm_workspace(M, K),), torch.uint8)
+    _check(_library().qlora_rmsnorm_bwd(dy, h, _TYPE[ht], w, _TYPE[weight.dtype], eps, dr, M, K,
+                                        _need(dH, "dH", (ht,), shape, dev), _opt(dX, "dX", (_BF16,), shape, dev),
+                                        _opt(dW, "dW", (_F32,), (K,), dev), *_space(ws, dev), call.handle),
+           "qlora_rmsnorm_bwd")
+    return dH, dX, dW
+
+
+def _space(ws, device):
+    if ws is None:
+        return None, 0
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous buffer on {device} is expected")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+def _adapter(act, act_name, w, w_name, act_shape, w_shape, device):
+    """Addresses and rank of an optional adapter term: both factors or neither."""
+    if act is None and w is None:
+        return None, None, 0
+    if act is None or w is None:
+        raise ValueError(f"{act_name} and {w_name} go together")
+    r = _matrix(act, act_name)[1]
+    return (_need(act, act_name, (_BF16,), act_shape(r), device), _need(w, w_name, (_BF16,), w_shape(r), device), r)
+
+
+def i8_linear_fwd(W: I8Matrix, X: I8Matrix, sU=None, B=None, Y=None, status=None, stream=None):
+    """Y [M, N] = (X codes . W codes^T) * X.scale * W.scale + sU B^T, bf16."""
+    M, K = xs = _matrix(X.codes, "X.codes")
+    N, _ = _matrix(W.codes, "W.codes")
+    dev = _device(X.codes, "X.codes")
+    call = _Call(stream, dev)
+    xq, sx = _need_i8(X, "X", xs, dev)
+    wq, sw = _need_i8(W, "W", (N, K), dev)
+    u, b, r = _adapter(sU, "sU", B, "B", lambda r: (M, r), lambda r: (N, r), dev)
+    if Y is None:
+        Y = call.empty((M, N), _BF16)
+    _check(_library().qlora_i8_linear_fwd(xq, sx, M, wq, sw, N, K, u, b, r, _need(Y, "Y", (_BF16,), (M, N), dev),
+                                          _opt(status, "status", (torch.int32,), (1,), dev), call.handle),
+           "qlora_i8_linear_fwd")
+    return Y
+
+
+def i8_linear_workspace(M: int, N: int, K: int) -> int:
+    b = ctypes.c_size_t()
+    _check(_library().qlora_i8_linear_workspace(M, N, K, ctypes.byref(b)), "qlora_i8_linear_workspace")
+    return b.value
+
+
+def i8_linear_dx(W: I8Matrix, dY, sT=None, A=None, dX=None, ws=None, status=None, stream=None):
+    """dX [M, K] of the 8-bit linear: int8 rows of dY * W.scale through W's codes, + sT A."""
+    M, N = ys = _matrix(dY, "dY")
+    _, K = _matrix(W.codes, "W.codes")
+    dev = _device(dY, "dY")
+    call = _Call(stream, dev)
+    dy = _need(dY, "dY", (_BF16,), ys, dev)
+    wq, sw = _need_i8(W, "W", (N, K), dev)
+    t, a, r = _adapter(sT, "sT", A, "A", lambda r: (M, r), lambda r: (r, K), dev)
+    if dX is None:
+        dX = call.empty((M, K), _BF16)
+    if ws is None:
+        ws = call.empty((i8_linear_workspace(M, N, K),), torch.uint8)
+    _check(_library().qlora_i8_linear_dx(dy, M, wq, sw, N, K, t, a, r, _need(dX, "dX", (_BF16,), (M, K), dev),
+                                         *_space(ws, dev), _opt(status, "status", (torch.int32,), (1,), dev),
+                                         call.handle), "qlora_i8_linear_dx")
+    return dX
