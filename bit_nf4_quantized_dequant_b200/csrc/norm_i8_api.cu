@@ -116,7 +116,7 @@ qlora_status_t qlora_i8_linear_fwd(const int8_t *Xq, const float *sx, int64_t M,
   a.lora_w = B;
   a.out = Y;
   a.status = dev_status;
-  return cuda_status(launch_i8_split(a, cu(stream)));
+  return cuda_status(launch_i8_gemm(a, cu(stream)));
 }
 
 qlora_status_t qlora_i8_linear_workspace(int64_t M, int64_t N, int64_t K, size_t *bytes) {
@@ -159,7 +159,7 @@ qlora_status_t qlora_i8_linear_dx(const uint16_t *dY, int64_t M, const int8_t *W
   a.lora_w = A;
   a.out = dX;
   a.status = dev_status;
-  return cuda_status(launch_i8_split(a, cu(stream)));
+  return cuda_status(launch_i8_gemm(a, cu(stream)));
 }
 
 }  // extern "C"

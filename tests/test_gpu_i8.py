@@ -88,6 +88,9 @@ LINEAR = [
     (17, 256, 256, 64), (33, 272, 144, 32), (64, 1024, 1024, 8), (100, 384, 640, 40), (128, 128, 2048, 48),
     (129, 528, 1040, 16), (200, 1008, 512, 56), (255, 256, 384, 0), (256, 256, 256, 16), (257, 272, 400, 8),
     (300, 4112, 80, 16), (513, 640, 768, 64), (700, 1040, 1296, 24), (1025, 384, 528, 16), (2047, 528, 272, 8),
+    # enough tiles for the SM pairs, each rank's template; then several tiles a pair
+    (2500, 1296, 1552, 0), (2305, 1552, 1296, 16), (3000, 1280, 1280, 8), (2400, 1360, 1424, 32), (2561, 1296, 1296, 40),
+    (2400, 1328, 1536, 64), (5000, 2064, 2320, 24), (4999, 2832, 144, 16), (4990, 144, 2576, 48), (13000, 272, 784, 8),
 ]
 
 
@@ -183,11 +186,11 @@ def test_results_do_not_depend_on_the_token_count(lib):
     whatever stands beside it (token tiles, splits and kernels differ): the
     integer sum is exact and the scales come in one order."""
     import torch
-    N, K = 656, 1040
-    xq, sx, wq, sw, _, _, dy, _, _ = _linear(torch, 1300, N, K, 0, 77)
+    N, K = 1296, 1328
+    xq, sx, wq, sw, _, _, dy, _, _ = _linear(torch, 3000, N, K, 0, 77)
     w, X, dy = _i8(lib, torch, wq, sw), _i8(lib, torch, xq, sx), dy.cuda()
     full, fullx = lib.i8_linear_fwd(w, X), lib.i8_linear_dx(w, dy)
-    for M in (1, 9, 40, 260, 600):
+    for M in (1, 9, 40, 260, 1200):
         one = lib.i8_linear_fwd(w, lib.I8Matrix(X.codes[:M], X.scale[:M]))
         assert torch.equal(one, full[:M]) and torch.equal(lib.i8_linear_dx(w, dy[:M]), fullx[:M]), M
 
