@@ -52,31 +52,33 @@ def _library():
     return _lib
 
 
-def _need(t, name, dtypes, shape, device):
-    """A contiguous CUDA tensor of one of these types and this shape, on `device`: its address."""
+def _need(t, name, dtype, shape, dev):
+    """A contiguous tensor of this type (or one of these) and shape on CUDA device `dev`: its address."""
+    if ((t.dtype is dtype or (dtype.__class__ is tuple and t.dtype in dtype)) and t.shape == shape
+            and t.get_device() == dev and t.is_contiguous()):
+        return t.data_ptr()
+    dtypes = dtype if isinstance(dtype, tuple) else (dtype,)
     if t.dtype not in dtypes:
         raise ValueError(f"{name}: {t.dtype}, expected {' or '.join(str(d) for d in dtypes)}")
     if t.shape != shape:
         raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.device != device:
-        raise ValueError(f"{name}: on {t.device}, expected {device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{dev}")
+    raise ValueError(f"{name}: not contiguous")
 
 
-def _opt(t, name, dtypes, shape, device):
-    return None if t is None else _need(t, name, dtypes, shape, device)
+def _opt(t, name, dtype, shape, dev):
+    return None if t is None else _need(t, name, dtype, shape, dev)
 
 
 def _device(t, name):
     """The device of a call: that of its first tensor, which has to be the current one."""
-    d = t.device
-    if d.type != "cuda":
-        raise ValueError(f"{name}: on {d}, expected a CUDA device")
-    if d.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {d}, but the current device is cuda:{torch.cuda.current_device()}")
-    return d
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name}: on {t.device}, expected a CUDA device")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+    return dev
 
 
 def _matrix(t, name):
@@ -85,24 +87,18 @@ def _matrix(t, name):
     return t.shape
 
 
-class _Call:
-    """The stream of a call, and the tensors allocated for it: memory comes from
-    the current stream's pool, so another stream's use of it is recorded."""
+def _raw(stream, dev):
+    """The handle of the stream to launch on: the given one, or the device's current one."""
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
-    __slots__ = ("other", "handle", "device")
 
-    def __init__(self, stream, device):
-        current = torch.cuda.current_stream()
-        self.other = stream if stream is not None and stream != current else None
-        self.handle = (self.other or current).cuda_stream
-        self.device = device
-
-    def empty(self, shape, dtype):
-        t = torch.empty(shape, dtype=dtype, device=self.device)
-        if self.other is not None:
-            self.other.wait_stream(torch.cuda.current_stream())   # the memory may still be in use there
-            t.record_stream(self.other)
-        return t
+def _empty(shape, dtype, dev, stream):
+    """Memory from the current stream's pool; where another stream uses it, that is recorded."""
+    t = torch.empty(shape, dtype=dtype, device=dev)
+    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev):
+        stream.wait_stream(torch.cuda.current_stream())   # the memory may still be in use here
+        t.record_stream(stream)
+    return t
 
 
 _check = _binding._check
@@ -120,22 +116,21 @@ class I8Matrix:
                    torch.empty(rows, dtype=_F32, device=device))
 
 
-def _need_i8(q, name, shape, device):
-    return (_need(q.codes, name + ".codes", (_I8,), shape, device),
-            _need(q.scale, name + ".scale", (_F32,), (shape[0],), device))
+def _need_i8(q, name, shape, dev):
+    return (_need(q.codes, name + ".codes", _I8, shape, dev),
+            _need(q.scale, name + ".scale", _F32, shape[:1], dev))
 
 
 def i8_quantize(X, col_scale=None, out: I8Matrix | None = None, stream=None) -> I8Matrix:
     """Int8 rows of X [M, K] (bf16 or fp32), or of X * col_scale[K]."""
     M, K = shape = _matrix(X, "X")
     dev = _device(X, "X")
-    call = _Call(stream, dev)
     x = _need(X, "X", (_BF16, _F32), shape, dev)
     if out is None:
-        out = I8Matrix(call.empty(shape, _I8), call.empty((M,), _F32))
+        out = I8Matrix(_empty(shape, _I8, dev, stream), _empty((M,), _F32, dev, stream))
     codes, scale = _need_i8(out, "out", shape, dev)
-    _check(_library().qlora_i8_quantize(x, _TYPE[X.dtype], M, K, _opt(col_scale, "col_scale", (_F32,), (K,), dev),
-                                        codes, scale, call.handle), "qlora_i8_quantize")
+    _check(_library().qlora_i8_quantize(x, _TYPE[X.dtype], M, K, _opt(col_scale, "col_scale", _F32, (K,), dev),
+                                        codes, scale, _raw(stream, dev)), "qlora_i8_quantize")
     return out
 
 
@@ -143,11 +138,10 @@ def i8_dequantize(q: I8Matrix, out=None, stream=None):
     """codes * scale as bf16 [M, K]."""
     M, K = shape = _matrix(q.codes, "codes")
     dev = _device(q.codes, "codes")
-    call = _Call(stream, dev)
     codes, scale = _need_i8(q, "q", shape, dev)
     if out is None:
-        out = call.empty(shape, _BF16)
-    _check(_library().qlora_i8_dequantize(codes, scale, M, K, _need(out, "out", (_BF16,), shape, dev), call.handle),
+        out = _empty(shape, _BF16, dev, stream)
+    _check(_library().qlora_i8_dequantize(codes, scale, M, K, _need(out, "out", _BF16, shape, dev), _raw(stream, dev)),
            "qlora_i8_dequantize")
     return out
 
@@ -163,19 +157,18 @@ def rmsnorm_fwd(X, weight, eps: float, residual=None, H=None, Y=None, q: I8Matri
         raise ValueError("X or residual is needed")
     M, K = shape = _matrix(first, "residual" if residual is not None else "X")
     dev = _device(first, "residual" if residual is not None else "X")
-    call = _Call(stream, dev)
     ht = _BF16 if residual is None else residual.dtype
-    x = _opt(X, "X", (_BF16,), shape, dev)
+    x = _opt(X, "X", _BF16, shape, dev)
     r = _opt(residual, "residual", (_BF16, _F32), shape, dev)
     w = _need(weight, "weight", (_BF16, _F32), (K,), dev)
     if Y is None and q is None:
-        Y = call.empty(shape, _BF16)
+        Y = _empty(shape, _BF16, dev, stream)
     if H is None and want_H and X is not None and residual is not None:
-        H = call.empty(shape, ht)
+        H = _empty(shape, ht, dev, stream)
     codes, scale = (None, None) if q is None else _need_i8(q, "q", shape, dev)
     _check(_library().qlora_rmsnorm_fwd(x, r, _TYPE[ht], w, _TYPE[weight.dtype], eps, M, K,
-                                        _opt(H, "H", (ht,), shape, dev), _opt(Y, "Y", (_BF16,), shape, dev),
-                                        codes, scale, call.handle), "qlora_rmsnorm_fwd")
+                                        _opt(H, "H", ht, shape, dev), _opt(Y, "Y", _BF16, shape, dev),
+                                        codes, scale, _raw(stream, dev)), "qlora_rmsnorm_fwd")
     return Y, H, q
 
 
@@ -191,41 +184,40 @@ def rmsnorm_bwd(dY, H, weight, eps: float, dres=None, dH=None, dX=None, dW=None,
     (only when dX is passed) and the weight's (fp32, or None without want_dW)."""
     M, K = shape = _matrix(dY, "dY")
     dev = _device(dY, "dY")
-    call = _Call(stream, dev)
     ht = H.dtype
-    dy = _need(dY, "dY", (_BF16,), shape, dev)
+    dy = _need(dY, "dY", _BF16, shape, dev)
     h = _need(H, "H", (_BF16, _F32), shape, dev)
     w = _need(weight, "weight", (_BF16, _F32), (K,), dev)
-    dr = _opt(dres, "dres", (ht,), shape, dev)
+    dr = _opt(dres, "dres", ht, shape, dev)
     if dH is None:
-        dH = call.empty(shape, ht)
+        dH = _empty(shape, ht, dev, stream)
     if dW is None and want_dW:
-        dW = call.empty((K,), _F32)
+        dW = _empty((K,), _F32, dev, stream)
     if dW is not None and ws is None:
-        ws = call.empty((rmsnorm_workspace(M, K),), torch.uint8)
+        ws = _empty((rmsnorm_workspace(M, K),), torch.uint8, dev, stream)
     _check(_library().qlora_rmsnorm_bwd(dy, h, _TYPE[ht], w, _TYPE[weight.dtype], eps, dr, M, K,
-                                        _need(dH, "dH", (ht,), shape, dev), _opt(dX, "dX", (_BF16,), shape, dev),
-                                        _opt(dW, "dW", (_F32,), (K,), dev), *_space(ws, dev), call.handle),
+                                        _need(dH, "dH", ht, shape, dev), _opt(dX, "dX", _BF16, shape, dev),
+                                        _opt(dW, "dW", _F32, (K,), dev), *_space(ws, dev), _raw(stream, dev)),
            "qlora_rmsnorm_bwd")
     return dH, dX, dW
 
 
-def _space(ws, device):
+def _space(ws, dev):
     if ws is None:
         return None, 0
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws: a contiguous buffer on {device} is expected")
+    if ws.get_device() != dev or not ws.is_contiguous():
+        raise ValueError(f"ws: a contiguous buffer on cuda:{dev} is expected")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _adapter(act, act_name, w, w_name, act_shape, w_shape, device):
+def _adapter(act, act_name, w, w_name, act_shape, w_shape, dev):
     """Addresses and rank of an optional adapter term: both factors or neither."""
     if act is None and w is None:
         return None, None, 0
     if act is None or w is None:
         raise ValueError(f"{act_name} and {w_name} go together")
     r = _matrix(act, act_name)[1]
-    return (_need(act, act_name, (_BF16,), act_shape(r), device), _need(w, w_name, (_BF16,), w_shape(r), device), r)
+    return (_need(act, act_name, _BF16, act_shape(r), dev), _need(w, w_name, _BF16, w_shape(r), dev), r)
 
 
 def i8_linear_fwd(W: I8Matrix, X: I8Matrix, sU=None, B=None, Y=None, status=None, stream=None):
@@ -233,14 +225,13 @@ def i8_linear_fwd(W: I8Matrix, X: I8Matrix, sU=None, B=None, Y=None, status=None
     M, K = xs = _matrix(X.codes, "X.codes")
     N, _ = _matrix(W.codes, "W.codes")
     dev = _device(X.codes, "X.codes")
-    call = _Call(stream, dev)
     xq, sx = _need_i8(X, "X", xs, dev)
     wq, sw = _need_i8(W, "W", (N, K), dev)
     u, b, r = _adapter(sU, "sU", B, "B", lambda r: (M, r), lambda r: (N, r), dev)
     if Y is None:
-        Y = call.empty((M, N), _BF16)
-    _check(_library().qlora_i8_linear_fwd(xq, sx, M, wq, sw, N, K, u, b, r, _need(Y, "Y", (_BF16,), (M, N), dev),
-                                          _opt(status, "status", (torch.int32,), (1,), dev), call.handle),
+        Y = _empty((M, N), _BF16, dev, stream)
+    _check(_library().qlora_i8_linear_fwd(xq, sx, M, wq, sw, N, K, u, b, r, _need(Y, "Y", _BF16, (M, N), dev),
+                                          _opt(status, "status", torch.int32, (1,), dev), _raw(stream, dev)),
            "qlora_i8_linear_fwd")
     return Y
 
@@ -256,15 +247,14 @@ def i8_linear_dx(W: I8Matrix, dY, sT=None, A=None, dX=None, ws=None, status=None
     M, N = ys = _matrix(dY, "dY")
     _, K = _matrix(W.codes, "W.codes")
     dev = _device(dY, "dY")
-    call = _Call(stream, dev)
-    dy = _need(dY, "dY", (_BF16,), ys, dev)
+    dy = _need(dY, "dY", _BF16, ys, dev)
     wq, sw = _need_i8(W, "W", (N, K), dev)
     t, a, r = _adapter(sT, "sT", A, "A", lambda r: (M, r), lambda r: (r, K), dev)
     if dX is None:
-        dX = call.empty((M, K), _BF16)
+        dX = _empty((M, K), _BF16, dev, stream)
     if ws is None:
-        ws = call.empty((i8_linear_workspace(M, N, K),), torch.uint8)
-    _check(_library().qlora_i8_linear_dx(dy, M, wq, sw, N, K, t, a, r, _need(dX, "dX", (_BF16,), (M, K), dev),
-                                         *_space(ws, dev), _opt(status, "status", (torch.int32,), (1,), dev),
-                                         call.handle), "qlora_i8_linear_dx")
+        ws = _empty((i8_linear_workspace(M, N, K),), torch.uint8, dev, stream)
+    _check(_library().qlora_i8_linear_dx(dy, M, wq, sw, N, K, t, a, r, _need(dX, "dX", _BF16, (M, K), dev),
+                                         *_space(ws, dev), _opt(status, "status", torch.int32, (1,), dev),
+                                         _raw(stream, dev)), "qlora_i8_linear_dx")
     return dX

@@ -61,6 +61,39 @@ __device__ __forceinline__ void umma_i8_pair(uint32_t tmem_d, uint64_t adesc, ui
       : "memory");
 }
 
+// 64 columns of 16 TMEM lanes as eight m16n8 accumulator fragments: of the n8
+// block j, thread T has columns 2 (T % 4), + 1 of lane T / 4 in r[4 j], r[4 j + 1]
+// and of lane T / 4 + 8 in r[4 j + 2], r[4 j + 3].
+__device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Two neighbouring ranks (k, k + 1) of the adapter's activations sU / sT at a
+// token, and of its weight at a feature: a register of an m16n8k16 fragment.
+// Ranks past r, tokens past M and features past F are zero.
+__device__ __forceinline__ uint32_t lora_act_pair(const uint16_t *u, int64_t M, int r, int64_t m, int k) {
+  return m < M && k < r ? __ldg(reinterpret_cast<const uint32_t *>(u + m * r + k)) : 0u;
+}
+template <bool kDx>
+__device__ __forceinline__ uint32_t lora_w_pair(const uint16_t *w, int64_t F, int r, int64_t f, int k) {
+  if (f >= F || k >= r) return 0u;
+  if constexpr (kDx) {   // A [r, F]
+    const uint16_t *a = w + static_cast<int64_t>(k) * F + f;
+    return static_cast<uint32_t>(__ldg(a)) | (static_cast<uint32_t>(__ldg(a + F)) << 16);
+  } else {               // B [F, r]
+    return __ldg(reinterpret_cast<const uint32_t *>(w + f * r + k));
+  }
+}
+
 // One load of a ring slot: waits (bounded) until a slot's copies have landed,
 // so that none outlives the CTA's shared memory after an abort.
 __device__ __forceinline__ void drain_slot(uint64_t *full, uint32_t parity) {

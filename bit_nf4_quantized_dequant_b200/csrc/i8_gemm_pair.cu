@@ -49,20 +49,6 @@ struct PairSmem {
   int abort_flag;
 };
 
-// 64 columns of 16 TMEM lanes as eight m16n8 accumulator fragments.
-__device__ __forceinline__ void tmem_ld_frag64(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(taddr)
-      : "memory");
-}
-
 __device__ __forceinline__ void stmatrix_x4(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b), "r"(c),
                "r"(d)
@@ -209,8 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
               const int k = ks * 16 + c * 8 + q2;
-              u[i >> 1][ks][(i & 1) + 2 * c] =
-                  m < p.M && k < p.r ? __ldg(reinterpret_cast<const uint32_t *>(p.lora_act + m * p.r + k)) : 0u;
+              u[i >> 1][ks][(i & 1) + 2 * c] = lora_act_pair(p.lora_act, p.M, p.r, m, k);
             }
         }
       }
@@ -241,20 +226,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int k = ks * 16 + c * 8 + q2;
-              const int64_t f = fc + j * 8 + g;
-              uint32_t v = 0u;
-              if (f < p.F && k < p.r) {
-                if constexpr (!kDx) {
-                  v = __ldg(reinterpret_cast<const uint32_t *>(p.lora_w + f * p.r + k));
-                } else {
-                  const uint16_t *a = p.lora_w + static_cast<int64_t>(k) * p.F + f;
-                  v = static_cast<uint32_t>(__ldg(a)) | (static_cast<uint32_t>(__ldg(a + p.F)) << 16);
-                }
-              }
-              b[j][c] = v;
-            }
+            for (int c = 0; c < 2; ++c)
+              b[j][c] = lora_w_pair<kDx>(p.lora_w, p.F, p.r, fc + j * 8 + g, ks * 16 + c * 8 + q2);
         };
         if constexpr (kSteps > 0) load_b(0);
         tmem_ld_wait();
@@ -369,10 +342,17 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
+// Single tiles of 128 x 128 as long as one wave of CTAs holds them; past that
+// the pairs' 256 x 256 tiles, which need half the operand bytes per output. A
+// little more than one wave of pairs goes back to single tiles, two to a SM.
+// Measured (rank 16): 512 tokens 4096 x 4096 (128 tiles, 32 pair tiles) 12.9 us
+// split, 16.3 pair; 768 tokens (192, 48) 20.2 and 17.4; 200 tokens 11008 x 4096
+// (172, 43) 21.1 and 18.5; 384 tokens (258, 86) 23.0 and 29.5.
 cudaError_t launch_i8_gemm(const I8GemmArgs &a, cudaStream_t st) {
-  // pair tiles once they fill at least two thirds of the SM pairs
-  const int64_t tiles = ((a.F + kTile - 1) / kTile) * ((a.M + kTile - 1) / kTile);
-  return tiles * 3 >= device_sm_count() ? launch_i8_pair(a, st) : launch_i8_split(a, st);
+  auto tiles = [&](int64_t t) { return ((a.F + t - 1) / t) * ((a.M + t - 1) / t); };
+  const int64_t sms = device_sm_count(), single = tiles(128);
+  const bool split = single <= sms || (single <= 2 * sms && tiles(kTile) > sms / 2);
+  return split ? launch_i8_split(a, st) : launch_i8_pair(a, st);
 }
 
 }  // namespace qlora

@@ -1,16 +1,21 @@
 // Int8 GEMM with the contraction split over a cluster: the kernel for token
-// counts that leave most SMs without an output tile of their own.
+// counts that leave most SM pairs without an output tile of their own.
 //
-// One CTA holds a tile of 128 features (UMMA M) by up to 256 tokens (UMMA N),
-// so a weight code is read once per 256 tokens; the CTAs of a cluster (1, 2, 4
-// or 8) take consecutive parts of the tile's contraction and their int32
-// partial sums are added over distributed shared memory. Integer sums are
-// exact, so the result does not depend on the split. Few tokens are bound by
-// the weight's bytes: the split brings enough CTAs to keep every SM loading,
-// and a ring of 128 x 128-code boxes up to 200 KB deep keeps them in flight.
+// One CTA holds a tile of 128 tokens (UMMA M) by 128 features (UMMA N); the
+// CTAs of a cluster (1 to 8) take consecutive parts of the tile's contraction
+// and their int32 partial sums are added over distributed shared memory.
+// Integer sums are exact, so the result does not depend on the split. Few
+// tokens are bound by the weight's bytes: the split brings enough CTAs to keep
+// every SM loading. A token box has only the rows that exist (rounded up to
+// 8): the MMA then reads past it into the weight box behind, which gives
+// integers in accumulator rows that nobody reads.
 //
-// Warps: 0 TMA producer, 1 MMA issuer and TMEM owner; 0-3 move the accumulator
-// from TMEM to shared memory (one lane per feature), all eight finish.
+// The accumulator is read in the fragment layout of the warp-level MMA (see
+// i8_gemm_pair.cu) and cut into blocks of 16 tokens x 16 features; the CTAs of
+// a cluster share the blocks that hold tokens, and each finishes its own:
+// sum, scales, adapter (mma.m16n8k16), bf16, 32-byte row segments stored.
+//
+// Warps: 0 TMA producer, 1 MMA issuer and TMEM owner; all eight finish.
 #include "i8_gemm.cuh"
 
 namespace qlora {
@@ -21,9 +26,10 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, ui
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFeat = 128;                                // features per tile
-constexpr uint32_t kWBytes = kFeat * kI8Step;             // weight box of a step
-constexpr int kMaxStages = 12;
+constexpr int kTile = 128;                                // tokens and features per tile
+constexpr uint32_t kWBytes = kTile * kI8Step;             // weight box of a step
+constexpr int kMaxStages = 10;
+constexpr int kMaxSplit = 8;
 
 struct SplitParams {
   const float *act_scale, *w_scale;
@@ -31,41 +37,97 @@ struct SplitParams {
   uint16_t *out;
   int32_t *status;
   int64_t M, F;
-  int r, tn, stages, nk, feat_tiles;
-  uint32_t tmem_cols;
+  int r, rows, stages, nk, feat_tiles, split;   // rows: tokens of an activation box
 };
 
-__host__ __device__ inline uint32_t ring_bytes(int tn, int stages) {
-  const uint32_t ring = static_cast<uint32_t>(stages) * (kWBytes + static_cast<uint32_t>(tn) * kI8Step);
-  const uint32_t part = static_cast<uint32_t>(tn) * kFeat * 4;
+__host__ __device__ inline uint32_t slot_bytes(int rows) { return kWBytes + static_cast<uint32_t>(rows) * kI8Step; }
+// the ring, later the partial sums: 16 x 16 blocks of 1 KiB, eight a row of blocks
+__host__ __device__ inline uint32_t ring_bytes(int rows, int stages, int split) {
+  const uint32_t ring = static_cast<uint32_t>(stages) * slot_bytes(rows);
+  const uint32_t part = split > 1 ? static_cast<uint32_t>((rows + 15) / 16) * 8u * 1024u : 0u;
   return ring > part ? ring : part;
 }
 
-__device__ __forceinline__ int2 ld_dsmem_int2(uint32_t addr) {
-  int2 v;
-  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+__device__ __forceinline__ int4 ld_dsmem_int4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
   return v;
 }
 
-template <bool kDx>
-__global__ void __launch_bounds__(kThreads, 1)
+// What a thread needs besides the sums to finish a block: the scales of its two
+// tokens and four features, and the adapter's fragments.
+template <bool kDx, int kSteps>
+struct BlockOperands {
+  float sx[2];
+  float2 sw[2];
+  uint32_t u[kSteps ? kSteps : 1][4];
+  uint32_t b[kSteps ? kSteps : 1][2][2];
+
+  __device__ __forceinline__ void load(const SplitParams &p, int64_t m0, int64_t f0, int lane) {
+    const int g = lane >> 2, q2 = (lane & 3) * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t m = m0 + g + 8 * i, f = f0 + 8 * i + q2;
+      sx[i] = m < p.M ? __ldg(p.act_scale + m) : 0.f;
+      sw[i] = make_float2(1.f, 1.f);
+      if (!kDx && f < p.F) sw[i] = __ldg(reinterpret_cast<const float2 *>(p.w_scale + f));
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const int k = ks * 16 + c * 8 + q2;
+          u[ks][i + 2 * c] = lora_act_pair(p.lora_act, p.M, p.r, m, k);
+          b[ks][i][c] = lora_w_pair<kDx>(p.lora_w, p.F, p.r, f0 + 8 * i + g, k);
+        }
+    }
+  }
+  // s: the block's sums, fragment by fragment
+  __device__ __forceinline__ void finish(const SplitParams &p, int64_t m0, int64_t f0, int lane, const int (&s)[8]) {
+    const int g = lane >> 2, q2 = (lane & 3) * 2;
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      float y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        y[e] = static_cast<float>(s[4 * j + e]) * sx[e >> 1];
+        if constexpr (!kDx) y[e] *= (e & 1) ? sw[j].y : sw[j].x;
+      }
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks) mma_16816(y, u[ks], b[ks][j][0], b[ks][j][1]);
+      const int64_t f = f0 + 8 * j + q2;
+      if (f < p.F) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int64_t m = m0 + g + 8 * i;
+          if (m < p.M) *reinterpret_cast<uint32_t *>(p.out + m * p.F + f) = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+        }
+      }
+    }
+  }
+};
+
+template <bool kDx, int kSteps>
+__global__ void __launch_bounds__(kThreads, 2)
     i8_split_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_act,
-                    const SplitParams p, const int split) {
+                    const SplitParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint16_t *lora = reinterpret_cast<uint16_t *>(ring + ring_bytes(p.tn, p.stages));   // [r][128]
-  uint64_t *full = reinterpret_cast<uint64_t *>(lora + static_cast<size_t>(p.r) * kFeat);
+  uint64_t *full = reinterpret_cast<uint64_t *>(ring + ring_bytes(p.rows, p.stages, p.split));
   uint64_t *empty = full + kMaxStages;
   uint64_t *done = empty + kMaxStages;
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(done + 1);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int split = p.split;
   const int rank = split > 1 ? static_cast<int>(cluster_ctarank()) : 0;
   const int tile = static_cast<int>(blockIdx.x) / split;
   const int ft = tile % p.feat_tiles, tt = tile / p.feat_tiles;
-  const int64_t f0 = static_cast<int64_t>(ft) * kFeat, t0 = static_cast<int64_t>(tt) * p.tn;
+  const int64_t f0 = static_cast<int64_t>(ft) * kTile, t0 = static_cast<int64_t>(tt) * kTile;
   const int s0 = p.nk * rank / split, s1 = p.nk * (rank + 1) / split;
-  const uint32_t act_bytes = static_cast<uint32_t>(p.tn) * kI8Step, slot_bytes = kWBytes + act_bytes;
+  const uint32_t act_bytes = static_cast<uint32_t>(p.rows) * kI8Step, slot_sz = slot_bytes(p.rows);
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -79,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_act);
   }
   if (warp == 1) {
-    tmem_alloc(tmem_holder, p.tmem_cols);
+    tmem_alloc(tmem_holder, kTile);
     tmem_relinquish();
   }
   tc_fence_before();
@@ -97,11 +159,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(&full[slot], slot_bytes);
-        uint8_t *w = ring + static_cast<uint32_t>(slot) * slot_bytes;
-        if (!kDx) tma_load_2d(w, &tm_w, &full[slot], s * kI8Step, static_cast<int32_t>(f0));
-        else      tma_load_2d(w, &tm_w, &full[slot], static_cast<int32_t>(f0), s * kI8Step);
-        tma_load_2d(w + kWBytes, &tm_act, &full[slot], s * kI8Step, static_cast<int32_t>(t0));
+        mbar_arrive_expect_tx(&full[slot], slot_sz);
+        uint8_t *x = ring + static_cast<uint32_t>(slot) * slot_sz;
+        tma_load_2d(x, &tm_act, &full[slot], s * kI8Step, static_cast<int32_t>(t0));
+        if (!kDx) tma_load_2d(x + act_bytes, &tm_w, &full[slot], s * kI8Step, static_cast<int32_t>(f0));
+        else      tma_load_2d(x + act_bytes, &tm_w, &full[slot], static_cast<int32_t>(f0), s * kI8Step);
         landed |= 1u << slot;
         par = (par & ~(1u << slot)) | (ph << slot);
         if (++slot == p.stages) {
@@ -115,11 +177,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 1) {
     if (elect_one()) {
-      const uint32_t idesc = idesc_i8(kFeat, static_cast<uint32_t>(p.tn), kDx, false);
+      constexpr uint32_t idesc = idesc_i8(kTile, kTile, false, kDx);
       // a step of 32 codes: +32 bytes along a K-major row, or 32 rows of 128 bytes (MN-major)
-      const uint64_t a0 = smem_desc(smem_u32(ring), kDx ? kWBytes : 16u, 1024u, kLayoutSW128);
-      const uint64_t b0 = smem_desc(smem_u32(ring) + kWBytes, 16u, 1024u, kLayoutSW128);
-      constexpr uint32_t a_step = (kDx ? 32u * 128u : 32u) >> 4;
+      const uint64_t a0 = smem_desc(smem_u32(ring), 16u, 1024u, kLayoutSW128);
+      const uint64_t b0 = smem_desc(smem_u32(ring) + act_bytes, kDx ? kWBytes : 16u, 1024u, kLayoutSW128);
+      constexpr uint32_t b_step = (kDx ? 32u * 128u : 32u) >> 4;
       int slot = 0;
       uint32_t ph = 0;
       bool ok = true;
@@ -129,10 +191,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        const uint64_t off = (static_cast<uint32_t>(slot) * slot_bytes) >> 4;
+        const uint64_t off = (static_cast<uint32_t>(slot) * slot_sz) >> 4;
 #pragma unroll
         for (uint32_t j = 0; j < kI8Step / 32; ++j)
-          umma_i8(tmem, a0 + off + j * a_step, b0 + off + j * 2u, idesc, s > s0 || j);
+          umma_i8(tmem, a0 + off + j * 2u, b0 + off + j * b_step, idesc, s > s0 || j);
         umma_commit(&empty[slot]);
         if (++slot == p.stages) {
           slot = 0;
@@ -143,85 +205,95 @@ __global__ void __launch_bounds__(kThreads, 1)
       umma_commit(done);
       if (!ok) drain_slot(done, 0);
     }
-  } else if (warp >= 4 && p.r) {
-    // the adapter's tile as [j][feature], while the main loop runs
-    for (int i = threadIdx.x - 128; i < p.r * kFeat; i += kThreads - 128) {
-      const int j = kDx ? i / kFeat : i % p.r, n = kDx ? i % kFeat : i / p.r;
-      uint16_t v = 0;
-      if (f0 + n < p.F) v = kDx ? p.lora_w[static_cast<int64_t>(j) * p.F + f0 + n] : p.lora_w[(f0 + n) * p.r + j];
-      lora[j * kFeat + n] = v;
-    }
   }
   __syncwarp();
 
-  // ---- accumulator -> shared memory [token][feature], over the finished ring ----
-  int *part = reinterpret_cast<int *>(ring);
-  if (warp < 4) {
+  // ---- this warp's part of the accumulator: tokens 32 quad .. + 31, features 64 half .. + 63 ----
+  const int quad = warp & 3, half = warp >> 2;
+  const int tokens = static_cast<int>(p.M - t0 < kTile ? p.M - t0 : kTile);
+  BlockOperands<kDx, kSteps> op;
+  if (split > 1) {
+    // blocks (row of blocks rb, column of blocks cb) that hold tokens, dealt out to the cluster's warps
+    const int blocks = (tokens + 15) / 16 * 8, step = split * (kThreads / 32);
+    int b = warp * split + rank;
+    if (b < blocks) op.load(p, t0 + (b >> 3) * 16, f0 + (b & 7) * 16, lane);   // under the main loop
+    int4 *part = reinterpret_cast<int4 *>(ring);   // [block][2][lane]
     // the TMEM loads are warp-wide: every lane takes the same way
     if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.status))) {
       tc_fence_after();
-      const int n = warp * 32 + lane;
-      for (int c = 0; c < p.tn; c += 16) {
-        uint32_t v[16];
-        asm volatile(
-            "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-            "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
-            : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-              "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-            : "r"(tmem + (static_cast<uint32_t>(warp * 32) << 16) + static_cast<uint32_t>(c))
-            : "memory");
-        tmem_ld_wait();
 #pragma unroll
-        for (int j = 0; j < 16; ++j) part[(c + j) * kFeat + n] = static_cast<int>(v[j]);
+      for (int h = 0; h < 2; ++h) {
+        if (quad * 32 + h * 16 < tokens) {
+          uint32_t v[32];
+          tmem_ld_frag64(tmem + (static_cast<uint32_t>(quad * 32 + h * 16) << 16) + half * 64, v);
+          tmem_ld_wait();
+          int4 *d = part + ((quad * 2 + h) * 8 + half * 4) * 64 + lane;
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            d[j * 32] = make_int4(static_cast<int>(v[4 * j]), static_cast<int>(v[4 * j + 1]),
+                                  static_cast<int>(v[4 * j + 2]), static_cast<int>(v[4 * j + 3]));
+        }
       }
       tc_fence_before();
     }
-  }
-  __syncwarp();
-  if (split > 1) cluster_sync_all();
-  else __syncthreads();
-
-  // ---- sum over the cluster, scales, adapter: this CTA's share of the tokens ----
-  if (!*abort_flag) {
-    const int per = (p.tn + split - 1) / split;
-    const int tb = rank * per, te = min(min(tb + per, p.tn), static_cast<int>(p.M - t0 < p.tn ? p.M - t0 : p.tn));
-    const int n = 2 * (threadIdx.x & 63);
-    if (f0 + n < p.F) {
-      const float w0 = kDx ? 1.f : p.w_scale[f0 + n], w1 = kDx ? 1.f : p.w_scale[f0 + n + 1];
-      uint32_t peer[8];
-      const uint32_t mine = smem_u32(part);
+    __syncwarp();
+    cluster_sync_all();
+    if (!*abort_flag) {
+      const uint32_t mine = smem_u32(part) + static_cast<uint32_t>(lane) * 16u;
+      for (; b < blocks; b += step) {
+        int s[8] = {};
 #pragma unroll
-      for (int q = 0; q < 8; ++q) peer[q] = q < split ? (split > 1 ? mapa_shared(mine, q) : mine) : 0u;
-      for (int t = tb + (threadIdx.x >> 6); t < te; t += kThreads / 64) {
-        int a0 = 0, a1 = 0;
-        const uint32_t off = static_cast<uint32_t>(t * kFeat + n) * 4u;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < kMaxSplit; ++q)
           if (q < split) {
-            const int2 v = ld_dsmem_int2(peer[q] + off);
-            a0 += v.x;
-            a1 += v.y;
+            const uint32_t at = mapa_shared(mine + static_cast<uint32_t>(b) * 1024u, static_cast<uint32_t>(q));
+            const int4 lo = ld_dsmem_int4(at), hi = ld_dsmem_int4(at + 512u);
+            s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
+            s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
           }
-        const int64_t m = t0 + t;
-        const float sx = p.act_scale[m];
-        float y0 = static_cast<float>(a0) * sx * w0, y1 = static_cast<float>(a1) * sx * w1;
-        const uint16_t *u = p.lora_act + m * p.r;
-        for (int j = 0; j < p.r; ++j) {
-          const float uj = __uint_as_float(static_cast<uint32_t>(u[j]) << 16);
-          const uint32_t b = *reinterpret_cast<const uint32_t *>(lora + j * kFeat + n);
-          y0 = fmaf(uj, __uint_as_float(b << 16), y0);
-          y1 = fmaf(uj, __uint_as_float(b & 0xffff0000u), y1);
-        }
-        *reinterpret_cast<uint32_t *>(p.out + m * p.F + f0 + n) = pack_bf16x2(y0, y1);
+        op.finish(p, t0 + (b >> 3) * 16, f0 + (b & 7) * 16, lane, s);
+        if (b + step < blocks) op.load(p, t0 + ((b + step) >> 3) * 16, f0 + ((b + step) & 7) * 16, lane);
       }
     }
+    // no CTA leaves while a peer may still read its partial sums
+    cluster_sync_all();
+  } else {
+    if (quad * 32 < tokens) op.load(p, t0 + quad * 32, f0 + half * 64, lane);   // under the main loop
+    if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.status))) {
+      tc_fence_after();
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const int64_t m0 = t0 + quad * 32 + h * 16;
+        if (quad * 32 + h * 16 >= tokens) break;
+        uint32_t v[32];
+        tmem_ld_frag64(tmem + (static_cast<uint32_t>(quad * 32 + h * 16) << 16) + half * 64, v);
+        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          int s[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s[e] = static_cast<int>(v[8 * c + e]);
+          if (h || c) op.load(p, m0, f0 + half * 64 + c * 16, lane);
+          op.finish(p, m0, f0 + half * 64 + c * 16, lane, s);
+        }
+      }
+      tc_fence_before();
+    }
+    __syncthreads();
   }
-  // no CTA leaves while a peer may still read its partial sums
-  if (split > 1) cluster_sync_all();
-  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    tmem_dealloc(tmem, p.tmem_cols);
+    tmem_dealloc(tmem, kTile);
+  }
+}
+
+template <bool kDx>
+const void *split_fn(int steps) {
+  switch (steps) {
+    case 0: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 0>);
+    case 1: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 1>);
+    case 2: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 2>);
+    case 3: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 3>);
+    default: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 4>);
   }
 }
 
@@ -238,44 +310,48 @@ cudaError_t launch_i8_split(const I8GemmArgs &a, cudaStream_t st) {
   p.M = a.M;
   p.F = a.F;
   p.r = a.r;
-  p.tn = a.M >= 256 ? 256 : static_cast<int>((a.M + 15) / 16 * 16);
-  p.tmem_cols = 32;
-  while (p.tmem_cols < static_cast<uint32_t>(p.tn)) p.tmem_cols *= 2;
+  p.rows = a.M >= kTile ? kTile : static_cast<int>((a.M + 7) / 8 * 8);
   p.nk = static_cast<int>((a.C + kI8Step - 1) / kI8Step);
-  p.feat_tiles = static_cast<int>((a.F + kFeat - 1) / kFeat);
-  const int64_t tiles = static_cast<int64_t>(p.feat_tiles) * ((a.M + p.tn - 1) / p.tn);
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= device_sm_count() && p.nk >= split * 2) split *= 2;
-  const int per_cta = (p.nk + split - 1) / split;
-  const uint32_t slot = kWBytes + static_cast<uint32_t>(p.tn) * kI8Step;
-  p.stages = static_cast<int>((200u * 1024u - static_cast<uint32_t>(p.r) * kFeat * 2u) / slot);
+  p.feat_tiles = static_cast<int>((a.F + kTile - 1) / kTile);
+  const int64_t tiles = static_cast<int64_t>(p.feat_tiles) * ((a.M + kTile - 1) / kTile);
+  // As many CTAs as there are SMs, each with about four steps or more. Measured
+  // with one token of 4096 x 4096 (32 tiles of 32 steps): 4 ways 6.3 us, 3 ways
+  // 6.7, 2 ways 7.2, 8 ways (two CTAs a SM) 7.2; 1024 x 4096: 8 ways 5.1, 4 ways 5.9.
+  // A cluster stays inside one of the eight GPCs, so a GPC's 18 SMs hold 18 / split of them.
+  const int gpc_sms = device_sm_count() / 8;
+  p.split = (p.nk + 3) / 4 < kMaxSplit ? (p.nk + 3) / 4 : kMaxSplit;
+  while (p.split > 1 && tiles > 8 * (gpc_sms / p.split)) --p.split;
+  const int per_cta = (p.nk + p.split - 1) / p.split;
+  // two CTAs a SM where there are more than SMs, else one with a deeper ring
+  const uint32_t room = (tiles * p.split > device_sm_count() ? 108u : 200u) * 1024u;
+  p.stages = static_cast<int>(room / slot_bytes(p.rows));
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   if (p.stages > per_cta) p.stages = per_cta;
-  const size_t smem = 1024 + ring_bytes(p.tn, p.stages) + static_cast<size_t>(p.r) * kFeat * 2 + (2 * kMaxStages + 1) * 8 + 16;
+  const size_t smem = 1024 + ring_bytes(p.rows, p.stages, p.split) + (2 * kMaxStages + 1) * 8 + 16;
 
   CUtensorMap tm_w, tm_act;
   const uint64_t wrow = static_cast<uint64_t>(a.dx ? a.F : a.C), wrows = static_cast<uint64_t>(a.dx ? a.C : a.F);
   bool ok = encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, wrow, wrows, wrow, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok &= encode_2d(&tm_act, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.act, a.C, a.M, a.C, kI8Step, p.tn,
+  ok &= encode_2d(&tm_act, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.act, a.C, a.M, a.C, kI8Step, p.rows,
                   CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return cudaErrorInvalidValue;
-  const void *fn = a.dx ? reinterpret_cast<const void *>(i8_split_kernel<true>)
-                        : reinterpret_cast<const void *>(i8_split_kernel<false>);
+  const int steps = (a.r + 15) / 16;
+  const void *fn = a.dx ? split_fn<true>(steps) : split_fn<false>(steps);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * split));
+  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void *args[] = {&tm_w, &tm_act, &p, &split};
+  void *args[] = {&tm_w, &tm_act, &p};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
