@@ -94,6 +94,19 @@ __device__ __forceinline__ uint32_t lora_w_pair(const uint16_t *w, int64_t F, in
   }
 }
 
+// Whether a phase is complete, without ever suspending the thread (try_wait may).
+__device__ __forceinline__ bool mbar_test_wait(uint64_t *bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
 // One load of a ring slot: waits (bounded) until a slot's copies have landed,
 // so that none outlives the CTA's shared memory after an abort.
 __device__ __forceinline__ void drain_slot(uint64_t *full, uint32_t parity) {

@@ -9,13 +9,20 @@
 //
 // The epilogue reads TMEM in the fragment layout of the warp-level MMA
 // (16x256b: a thread holds two neighbouring features of rows T / 4 and
-// T / 4 + 8), scales to fp32 and adds the adapter's term by mma.m16n8k16 into
-// the same registers: the rank-r product needs neither a second accumulator nor
-// more than r / 8 warp MMAs per 16 x 8 outputs. bf16 results leave through
-// swizzled shared memory and TMA stores, which clip the ragged edges.
+// T / 4 + 8), scales to fp32, packs bf16 and stores through swizzled shared
+// memory by TMA, which clips the ragged edges.
 //
-// Warps (384 threads): 0 TMA producer, 1 MMA issuer and TMEM owner, 4-11
-// epilogue (TMEM lane quadrant warp % 4, half of the columns each).
+// With an adapter the scaled fp32 sums go back to the TMEM columns they came
+// from; one bf16 MMA per 16 ranks then adds sU B^T (or sT A) in place, and a
+// second read takes the finished values. The issuer slips that MMA in between
+// the next tile's steps, so only the epilogue waits for it. Adding the term by
+// warp-level MMAs in the epilogue instead stalls the tcgen05 stream, which
+// shares the tensor cores: 4096 tokens 14336 x 4096 took 152 us without an
+// adapter, 176 at rank 16 and 273 at rank 64.
+//
+// Warps (384 threads): 0 TMA producer, 1 MMA issuer and TMEM owner, 2 adapter
+// producer, 4-11 epilogue (TMEM lane quadrant warp % 4, half of the columns
+// each).
 #include "i8_gemm.cuh"
 
 namespace qlora {
@@ -29,25 +36,43 @@ constexpr int kThreads = 384;
 constexpr int kTile = 256;                                 // tokens and features per pair tile
 constexpr uint32_t kBoxBytes = 128 * kI8Step;              // 16 KiB: 128 tokens, or 128 features, of a step
 constexpr uint32_t kSlotBytes = 2 * kBoxBytes;
-constexpr int kStages = 6;
-constexpr uint32_t kOutBytes = 32 * 128;                   // 32 tokens x 64 features bf16, per epilogue warp
+constexpr int kMaxStages = 6;
+constexpr uint32_t kOutBytes = 16 * 128;                   // 16 tokens x 64 features bf16, per epilogue warp
 constexpr int kEpiWarps = 8;
 
 struct PairParams {
   const float *act_scale, *w_scale;
-  const uint16_t *lora_act, *lora_w;
   int32_t *status;
   int64_t M, F;
-  int r, nk, feat_tiles, tok_tiles;
+  int r_pad, stages;   // adapter ranks in shared memory (0, 16, 32 or 64), ring depth
+  int nk, feat_tiles, tok_tiles;
 };
 
-struct PairSmem {
-  uint8_t ring[kStages][kSlotBytes];
-  uint8_t out[kEpiWarps][kOutBytes];
-  uint64_t full[kStages], empty[kStages], accf[2], acce[2], drain;
+// Shared memory: ring, epilogue staging, the adapter's two tiles (128 tokens
+// and 128 features of r_pad ranks, bf16), barriers.
+struct PairBars {
+  uint64_t full[kMaxStages], empty[kMaxStages], accf[2], acce[2], loraf, lorae, scaled, added, drain;
   uint32_t tmem_holder;
   int abort_flag;
 };
+__host__ __device__ inline uint32_t lora_bytes(int r_pad) { return 128u * static_cast<uint32_t>(r_pad) * 2u; }
+__host__ __device__ inline uint32_t bars_offset(int stages, int r_pad) {
+  return static_cast<uint32_t>(stages) * kSlotBytes + kEpiWarps * kOutBytes + 2u * lora_bytes(r_pad);
+}
+
+// The reverse of tmem_ld_frag64.
+__device__ __forceinline__ void tmem_st_frag64(uint32_t taddr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
+      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void stmatrix_x4(uint32_t saddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(a), "r"(b), "r"(c),
@@ -55,13 +80,16 @@ __device__ __forceinline__ void stmatrix_x4(uint32_t saddr, uint32_t a, uint32_t
                : "memory");
 }
 
-// kSteps: mma steps of 16 ranks (0: no adapter).
-template <bool kDx, int kSteps>
+template <bool kDx, bool kLora>
 __global__ void __launch_bounds__(kThreads, 1)
     i8_pair_kernel(const __grid_constant__ CUtensorMap tm_w, const __grid_constant__ CUtensorMap tm_act,
-                   const __grid_constant__ CUtensorMap tm_out, const PairParams p) {
+                   const __grid_constant__ CUtensorMap tm_out, const __grid_constant__ CUtensorMap tm_lora_w,
+                   const __grid_constant__ CUtensorMap tm_lora_act, const PairParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
-  PairSmem &sm = *reinterpret_cast<PairSmem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t *out_stage = ring + static_cast<uint32_t>(p.stages) * kSlotBytes;
+  uint8_t *lora_a = out_stage + kEpiWarps * kOutBytes, *lora_b = lora_a + lora_bytes(p.r_pad);
+  PairBars &sm = *reinterpret_cast<PairBars *>(ring + bars_offset(p.stages, p.r_pad));
   volatile int *abort_flag = &sm.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -73,7 +101,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto feat0 = [&](int tile) { return (tile / p.tok_tiles) * kTile; };
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < kStages; ++i) {
+    for (int i = 0; i < p.stages; ++i) {
       mbar_init(&sm.full[i], 1);
       mbar_init(&sm.empty[i], 1);
     }
@@ -81,12 +109,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sm.accf[i], 1);
       mbar_init(&sm.acce[i], 2 * kEpiWarps);
     }
+    mbar_init(&sm.loraf, 1);
+    mbar_init(&sm.lorae, 1);
+    mbar_init(&sm.scaled, 2 * kEpiWarps);
+    mbar_init(&sm.added, 1);
     mbar_init(&sm.drain, 1);
     sm.abort_flag = 0;
     fence_mbarrier_init();
     tma_prefetch_desc(&tm_w);
     tma_prefetch_desc(&tm_act);
     tma_prefetch_desc(&tm_out);
+    if (kLora) {
+      tma_prefetch_desc(&tm_lora_w);
+      tma_prefetch_desc(&tm_lora_act);
+    }
   }
   if (warp == 1) {
     tmem_alloc_pair(&sm.tmem_holder, 512);
@@ -113,30 +149,72 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           if (leader) mbar_arrive_expect_tx(&sm.full[slot], 2 * kSlotBytes);
           const uint32_t bar = mapa_shared(smem_u32(&sm.full[slot]), 0u);
-          tma_load_2d_pair(sm.ring[slot], &tm_act, bar, s * kI8Step, t0);
-          if (!kDx) tma_load_2d_pair(sm.ring[slot] + kBoxBytes, &tm_w, bar, s * kI8Step, f0);
-          else      tma_load_2d_pair(sm.ring[slot] + kBoxBytes, &tm_w, bar, f0, s * kI8Step);
+          uint8_t *x = ring + static_cast<uint32_t>(slot) * kSlotBytes;
+          tma_load_2d_pair(x, &tm_act, bar, s * kI8Step, t0);
+          if (!kDx) tma_load_2d_pair(x + kBoxBytes, &tm_w, bar, s * kI8Step, f0);
+          else      tma_load_2d_pair(x + kBoxBytes, &tm_w, bar, f0, s * kI8Step);
           landed |= 1u << slot;
           par = (par & ~(1u << slot)) | (ph << slot);
-          if (++slot == kStages) {
+          if (++slot == p.stages) {
             slot = 0;
             ph ^= 1u;
           }
         }
       }
       if (!ok && leader)
-        for (int i = 0; i < kStages; ++i)
+        for (int i = 0; i < p.stages; ++i)
           if (landed & (1u << i)) drain_slot(&sm.full[i], (par >> i) & 1u);
+    }
+  } else if (warp == 2) {
+    // ---------------- adapter producer: this CTA's tokens and features, once a tile ----------------
+    if (kLora && elect_one()) {
+      bool issued = false, ok = true;
+      uint32_t ph = 0;
+      const uint32_t bar = mapa_shared(smem_u32(&sm.loraf), 0u);
+      for (int tile = first; tile < ntiles; tile += stride, ph ^= 1u) {
+        if (!mbar_wait(&sm.lorae, ph ^ 1u, abort_flag, p.status)) {
+          ok = false;
+          break;
+        }
+        const int t0 = tok0(tile) + static_cast<int>(rank) * 128, f0 = feat0(tile) + static_cast<int>(rank) * 128;
+        if (leader) mbar_arrive_expect_tx(&sm.loraf, 4 * lora_bytes(p.r_pad));
+        tma_load_2d_pair(lora_a, &tm_lora_act, bar, 0, t0);
+        if (!kDx) {
+          tma_load_2d_pair(lora_b, &tm_lora_w, bar, 0, f0);
+        } else {
+          tma_load_2d_pair(lora_b, &tm_lora_w, bar, f0, 0);
+          tma_load_2d_pair(lora_b + 128u * p.r_pad, &tm_lora_w, bar, f0 + 64, 0);
+        }
+        issued = true;
+      }
+      if (!ok && issued && leader) drain_slot(&sm.loraf, ph ^ 1u);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer (even CTA) ----------------
     if (leader && elect_one()) {
       constexpr uint32_t idesc = idesc_i8(256, kTile, false, kDx);
-      const uint64_t a0 = smem_desc(smem_u32(sm.ring[0]), 16u, 1024u, kLayoutSW128);
-      const uint64_t b0 = smem_desc(smem_u32(sm.ring[0]) + kBoxBytes, kDx ? kBoxBytes : 16u, 1024u, kLayoutSW128);
+      const uint64_t a0 = smem_desc(smem_u32(ring), 16u, 1024u, kLayoutSW128);
+      const uint64_t b0 = smem_desc(smem_u32(ring) + kBoxBytes, kDx ? kBoxBytes : 16u, 1024u, kLayoutSW128);
       // a step of 32 codes: +32 bytes along a K-major row, or 32 rows of 128 bytes (MN-major)
       constexpr uint32_t b_step = (kDx ? 32u * 128u : 32u) >> 4;
-      int slot = 0, n = 0;
+      // The adapter's MMAs into the scaled accumulator of the pair's tile i.
+      const uint32_t span = 2u * static_cast<uint32_t>(p.r_pad);   // bytes of a K-major row of ranks
+      const uint32_t lsw = span == 32u ? kLayoutSW32 : (span == 64u ? kLayoutSW64 : kLayoutSW128);
+      auto add_lora = [&](int i) -> bool {
+        if (!mbar_wait(&sm.loraf, static_cast<uint32_t>(i) & 1u, abort_flag, p.status)) return false;
+        tc_fence_after();
+        constexpr uint32_t lidesc = idesc_bf16(256, kTile, false, kDx);
+        for (uint32_t j = 0; j < static_cast<uint32_t>(p.r_pad) / 16u; ++j) {
+          const uint64_t ad = smem_desc(smem_u32(lora_a) + 32u * j, 16u, 8u * span, lsw);
+          const uint64_t bd = kDx ? smem_desc(smem_u32(lora_b) + 2048u * j, 64u * span, 1024u, kLayoutSW128)
+                                  : smem_desc(smem_u32(lora_b) + 32u * j, 16u, 8u * span, lsw);
+          umma_bf16_pair(tmem + static_cast<uint32_t>(i & 1) * kTile, ad, bd, lidesc, 1u);
+        }
+        umma_commit_pair(&sm.lorae);
+        umma_commit_pair(&sm.added);
+        return true;
+      };
+      int slot = 0, n = 0, added = 0;   // added: tiles whose adapter term is issued
       uint32_t ph = 0;
       bool ok = true;
       for (int tile = first; tile < ntiles && ok; tile += stride, ++n) {
@@ -148,6 +226,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const uint32_t d = tmem + static_cast<uint32_t>(buf) * kTile;
         for (int s = 0; s < p.nk; ++s) {
+          if (kLora && added < n && mbar_test_wait(&sm.scaled, static_cast<uint32_t>(added) & 1u)) {
+            if (!add_lora(added++)) {
+              ok = false;
+              break;
+            }
+          }
           if (!mbar_wait(&sm.full[slot], ph, abort_flag, p.status)) {
             ok = false;
             break;
@@ -158,12 +242,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (uint32_t j = 0; j < kI8Step / 32; ++j)
             umma_i8_pair(d, a0 + off + j * 2u, b0 + off + j * b_step, idesc, s || j);
           umma_commit_pair(&sm.empty[slot]);
-          if (++slot == kStages) {
+          if (++slot == p.stages) {
             slot = 0;
             ph ^= 1u;
           }
         }
-        if (ok) umma_commit_pair(&sm.accf[buf]);
+        if (!ok) break;
+        umma_commit_pair(&sm.accf[buf]);
+        // the previous tile's term is due before its accumulator can be had again; after the last tile, its own too
+        if (kLora)
+          for (const int due = tile + stride < ntiles ? n : n + 1; added < due && ok;)
+            ok = mbar_wait(&sm.scaled, static_cast<uint32_t>(added) & 1u, abort_flag, p.status) && add_lora(added++);
       }
       if (!ok) {   // the MMAs issued so far must be over before the CTA leaves
         umma_commit_pair(&sm.drain);
@@ -173,47 +262,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
     const int quad = warp & 3, half = (warp - 4) >> 2;   // 32 tokens, 128 features of the CTA's 128 x 256
-    uint8_t *stage = sm.out[warp - 4];
-    const uint32_t stage_a = smem_u32(stage);
+    uint8_t *stage = out_stage + static_cast<uint32_t>(warp - 4) * kOutBytes;
     const int g = lane >> 2, q2 = (lane & 3) * 2;        // fragment row and column pair
+    const uint32_t st_row = lane & 15, st_chunk = lane >> 4;   // this lane's stmatrix row and first 16-byte chunk
+    const uint32_t st_addr = smem_u32(stage) + st_row * 128u;
+    const uint32_t t_warp = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
     int n = 0;
     bool ok = true;
     for (int tile = first; tile < ntiles && ok; tile += stride, ++n) {
       const int buf = n & 1;
       const int64_t m0 = static_cast<int64_t>(tok0(tile)) + rank * 128 + quad * 32;
       const int64_t f0 = static_cast<int64_t>(feat0(tile)) + half * 128;
-      // this thread's four tokens: scales and adapter fragments, ahead of the accumulator
-      float sx[4];
-      uint32_t u[2][kSteps ? kSteps : 1][4];
+      const uint32_t t_acc = t_warp + buf * kTile;
+      float sx[4];   // tokens g, g + 8, g + 16, g + 24
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int64_t m = m0 + g + 8 * i;
-        sx[i] = m < p.M ? __ldg(p.act_scale + m) : 0.f;
-        if constexpr (kSteps > 0) {
-#pragma unroll
-          for (int ks = 0; ks < kSteps; ++ks)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              const int k = ks * 16 + c * 8 + q2;
-              u[i >> 1][ks][(i & 1) + 2 * c] = lora_act_pair(p.lora_act, p.M, p.r, m, k);
-            }
-        }
-      }
+      for (int i = 0; i < 4; ++i) sx[i] = m0 + g + 8 * i < p.M ? __ldg(p.act_scale + m0 + g + 8 * i) : 0.f;
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.accf[buf], (n >> 1) & 1u, abort_flag, p.status))) {
         ok = false;
         break;
       }
       tc_fence_after();
-#pragma unroll 1
-      for (int ch = 0; ch < 2; ++ch) {
-        const int64_t fc = f0 + ch * 64;
-        uint32_t acc[2][32];
-        const uint32_t ta = tmem + (static_cast<uint32_t>(quad * 32) << 16) + buf * kTile + half * 128 + ch * 64;
-        tmem_ld_frag64(ta, acc[0]);
-        tmem_ld_frag64(ta + (16u << 16), acc[1]);
-        float y[2][8][4];
-        // feature scales of this thread's columns, under the TMEM loads
-        float2 sw[8];
+      // sums to scaled fp32, in the thread's 2 x 16 values of 64 features by 16 tokens (h: which 16)
+      auto scale = [&](uint32_t (&v)[32], const float2 (&sw)[8], int h) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            float y = static_cast<float>(static_cast<int>(v[4 * j + e])) * (h ? sx[2 + (e >> 1)] : sx[e >> 1]);
+            if constexpr (!kDx) y *= (e & 1) ? sw[j].y : sw[j].x;
+            v[4 * j + e] = __float_as_uint(y);
+          }
+      };
+      auto load_sw = [&](float2 (&sw)[8], int64_t fc) {
         if constexpr (!kDx) {
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
@@ -221,15 +301,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             sw[j] = f < p.F ? __ldg(reinterpret_cast<const float2 *>(p.w_scale + f)) : make_float2(0.f, 0.f);
           }
         }
-        uint32_t b[kSteps ? 8 : 1][2];
-        auto load_b = [&](int ks) {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int c = 0; c < 2; ++c)
-              b[j][c] = lora_w_pair<kDx>(p.lora_w, p.F, p.r, fc + j * 8 + g, ks * 16 + c * 8 + q2);
-        };
-        if constexpr (kSteps > 0) load_b(0);
+      };
+      if constexpr (kLora) {
+#pragma unroll 1
+        for (int ch = 0; ch < 2; ++ch) {
+          float2 sw[8];
+          uint32_t v[2][32];
+          tmem_ld_frag64(t_acc + ch * 64, v[0]);
+          tmem_ld_frag64(t_acc + ch * 64 + (16u << 16), v[1]);
+          load_sw(sw, f0 + ch * 64);
+          tmem_ld_wait();
+          scale(v[0], sw, 0);
+          tmem_st_frag64(t_acc + ch * 64, v[0]);
+          scale(v[1], sw, 1);
+          tmem_st_frag64(t_acc + ch * 64 + (16u << 16), v[1]);
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.scaled), 0u));
+        if (!__all_sync(0xffffffffu, mbar_wait(&sm.added, static_cast<uint32_t>(n) & 1u, abort_flag, p.status))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int ch = 0; ch < 2; ++ch) {
+        const int64_t fc = f0 + ch * 64;
+        float2 sw[8];
+        uint32_t v[2][32];
+        tmem_ld_frag64(t_acc + ch * 64, v[0]);
+        tmem_ld_frag64(t_acc + ch * 64 + (16u << 16), v[1]);
+        if constexpr (!kLora) load_sw(sw, fc);
         tmem_ld_wait();
         if (ch == 1) {   // the accumulator is in registers: the next tile but one may have it
           tc_fence_before();
@@ -237,43 +341,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.acce[buf]), 0u));
         }
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float v = static_cast<float>(static_cast<int>(acc[h][4 * j + e])) * sx[2 * h + (e >> 1)];
-              if constexpr (!kDx) v *= (e & 1) ? sw[j].y : sw[j].x;
-              y[h][j][e] = v;
-            }
-        if constexpr (kSteps > 0) {
-#pragma unroll
-          for (int ks = 0; ks < kSteps; ++ks) {
-            if (ks) load_b(ks);
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-              for (int j = 0; j < 8; ++j) mma_16816(y[h][j], u[h][ks], b[j][0], b[j][1]);
-          }
-        }
-        // the staging tile is free again once the previous store has read it
-        if (lane == 0) bulk_wait_group_read<0>();
-        __syncwarp();
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h) {
+          if constexpr (!kLora) scale(v[h], sw, h);
+          // the staging tile is free again once the previous store has read it
+          if (lane == 0) bulk_wait_group_read<0>();
+          __syncwarp();
 #pragma unroll
           for (int j = 0; j < 8; j += 2) {
-            const uint32_t row = static_cast<uint32_t>(h * 16 + ((lane >> 3) & 1) * 8 + (lane & 7));
-            const uint32_t chunk = static_cast<uint32_t>(j + (lane >> 4));
-            stmatrix_x4(stage_a + row * 128u + ((chunk ^ (row & 7u)) << 4), pack_bf16x2(y[h][j][0], y[h][j][1]),
-                        pack_bf16x2(y[h][j][2], y[h][j][3]), pack_bf16x2(y[h][j + 1][0], y[h][j + 1][1]),
-                        pack_bf16x2(y[h][j + 1][2], y[h][j + 1][3]));
+            auto pack = [&](int i) { return pack_bf16x2(__uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1])); };
+            stmatrix_x4(st_addr + (((j + st_chunk) ^ (st_row & 7u)) << 4), pack(4 * j), pack(4 * j + 2), pack(4 * j + 4),
+                        pack(4 * j + 6));
           }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && m0 < p.M && fc < p.F) {
-          tma_store_2d(&tm_out, stage, static_cast<int32_t>(fc), static_cast<int32_t>(m0));
-          bulk_commit_group();
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0 && m0 + h * 16 < p.M && fc < p.F) {
+            tma_store_2d(&tm_out, stage, static_cast<int32_t>(fc), static_cast<int32_t>(m0 + h * 16));
+            bulk_commit_group();
+          }
         }
       }
     }
@@ -288,14 +372,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 template <bool kDx>
-const void *pair_fn(int steps) {
-  switch (steps) {
-    case 0: return reinterpret_cast<const void *>(i8_pair_kernel<kDx, 0>);
-    case 1: return reinterpret_cast<const void *>(i8_pair_kernel<kDx, 1>);
-    case 2: return reinterpret_cast<const void *>(i8_pair_kernel<kDx, 2>);
-    case 3: return reinterpret_cast<const void *>(i8_pair_kernel<kDx, 3>);
-    default: return reinterpret_cast<const void *>(i8_pair_kernel<kDx, 4>);
-  }
+const void *pair_fn(bool lora) {
+  return lora ? reinterpret_cast<const void *>(i8_pair_kernel<kDx, true>)
+              : reinterpret_cast<const void *>(i8_pair_kernel<kDx, false>);
 }
 
 }  // namespace
@@ -304,25 +383,33 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
   PairParams p{};
   p.act_scale = a.act_scale;
   p.w_scale = a.w_scale;
-  p.lora_act = a.lora_act;
-  p.lora_w = a.lora_w;
   p.status = a.status;
   p.M = a.M;
   p.F = a.F;
-  p.r = a.r;
+  p.r_pad = a.r == 0 ? 0 : (a.r <= 16 ? 16 : (a.r <= 32 ? 32 : 64));
+  p.stages = p.r_pad <= 32 ? 6 : 5;   // what 227 KB hold beside the adapter's tiles
   p.nk = static_cast<int>((a.C + kI8Step - 1) / kI8Step);
   p.feat_tiles = static_cast<int>((a.F + kTile - 1) / kTile);
   p.tok_tiles = static_cast<int>((a.M + kTile - 1) / kTile);
 
-  CUtensorMap tm_w, tm_act, tm_out;
+  CUtensorMap tm_w, tm_act, tm_out, tm_lora_w, tm_lora_act;
   const uint64_t wrow = static_cast<uint64_t>(a.dx ? a.F : a.C), wrows = static_cast<uint64_t>(a.dx ? a.C : a.F);
   bool ok = encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, wrow, wrows, wrow, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
   ok &= encode_2d(&tm_act, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.act, a.C, a.M, a.C, kI8Step, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok &= encode_2d(&tm_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.F, a.M, a.F * 2, 64, 32, CU_TENSOR_MAP_SWIZZLE_128B);
+  ok &= encode_2d(&tm_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.F, a.M, a.F * 2, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B);
+  tm_lora_w = tm_lora_act = tm_out;
+  if (a.r) {
+    const CUtensorMapSwizzle sw = p.r_pad == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
+                                  : p.r_pad == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                                                  : CU_TENSOR_MAP_SWIZZLE_128B;
+    ok &= encode_2d(&tm_lora_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_act, a.r, a.M, a.r * 2, p.r_pad, 128, sw);
+    ok &= a.dx ? encode_2d(&tm_lora_w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_w, a.F, a.r, a.F * 2, 64, p.r_pad,
+                           CU_TENSOR_MAP_SWIZZLE_128B)
+               : encode_2d(&tm_lora_w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_w, a.r, a.F, a.r * 2, p.r_pad, 128, sw);
+  }
   if (!ok) return cudaErrorInvalidValue;
-  const int steps = (a.r + 15) / 16;
-  const void *fn = a.dx ? pair_fn<true>(steps) : pair_fn<false>(steps);
-  const size_t smem = sizeof(PairSmem) + 1024;
+  const void *fn = a.dx ? pair_fn<true>(a.r != 0) : pair_fn<false>(a.r != 0);
+  const size_t smem = 1024 + bars_offset(p.stages, p.r_pad) + sizeof(PairBars);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.feat_tiles) * p.tok_tiles, pairs = device_sm_count() / 2;
@@ -338,7 +425,7 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  void *args[] = {&tm_w, &tm_act, &tm_out, &p};
+  void *args[] = {&tm_w, &tm_act, &tm_out, &tm_lora_w, &tm_lora_act, &p};
   return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
