@@ -4,166 +4,171 @@
 //   code = rint(fp32_rn(v / s)) clamped to +-127.
 //
 // Both are bound by memory (2 to 4 bytes read and 1 written an element), so a
-// row is read once and kept in registers between its maximum and its codes.
+// row is read once and kept in registers, as it was loaded, between its maximum
+// and its codes.
 #include "norm_i8.h"
 #include "row_device.cuh"
 
 namespace qlora {
 namespace {
 
-// A row per warp (WARP) or per block; a thread holds NV vectors of VEC
-// elements: element (i * T + t) * VEC of thread t.
-template <int VEC, int NV, bool WARP, bool F32>
-__global__ void __launch_bounds__(WARP ? 256 : 1024)
-    i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int64_t K,
+template <bool F32, bool ALIGNED>
+__device__ __forceinline__ void scaled(float (&f)[8], const Vec8<F32> &v, const float *col_scale, int e, int K) {
+  v.get(f);
+  if (col_scale) {
+    float c[8];
+    load_cols<ALIGNED, true>(c, col_scale, e, K);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], c[j]);
+  }
+}
+
+// A row per warp (WARP) or per block; vector i * T + t belongs to thread t.
+template <int NV, bool WARP, bool ALIGNED, bool F32>
+__global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 1 || NV == 8 ? 1 : (F32 ? 2 : 3)))
+    i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int K,
                        int8_t *__restrict__ codes, float *__restrict__ scale) {
   __shared__ uint32_t slot[32];
   const int T = WARP ? 32 : blockDim.x;
   const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
   const int64_t m = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && m >= M) return;
-  const void *row = F32 ? static_cast<const void *>(static_cast<const float *>(X) + m * K)
-                        : static_cast<const void *>(static_cast<const uint16_t *>(X) + m * K);
-  float f[NV][VEC];
-  uint32_t mx = 0;
+  const void *row = row_at<F32>(X, m * K);
+  const int phase = ALIGNED ? 0 : static_cast<int>((m * K) & 7);
+  Vec8<F32> v[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) v[i].template load<ALIGNED>(row, (i * T + t) * 8 - phase, K);
+  float mx = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t k = static_cast<int64_t>(i * T + t) * VEC;
-    if (k < K) {
-      load_row<VEC, F32>(f[i], row, k);
-    } else {
+    float f[8];
+    scaled<F32, ALIGNED>(f, v[i], col_scale, (i * T + t) * 8 - phase, K);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) f[i][j] = 0.f;
-    }
+    for (int j = 0; j < 8; ++j) mx = max_mag(mx, f[j]);
   }
-  if (col_scale) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int64_t k = static_cast<int64_t>(i * T + t) * VEC;
-      if (k < K) {
-        float c[VEC];
-        load_row<VEC, true>(c, col_scale, k);
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) f[i][j] = __fmul_rn(f[i][j], c[j]);
-      }
-    }
-  }
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) mx = max(mx, mag_bits(f[i][j]));
-  const RowScale rs = row_scale(row_max<WARP>(mx, slot));
+  const RowScale rs = row_scale(row_max<WARP>(__float_as_uint(mx), slot));
   if (t == 0) scale[m] = rs.s;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int64_t k = static_cast<int64_t>(i * T + t) * VEC;
-    if (k < K) store_codes<VEC>(f[i], rs, codes + m * K, k);
+    const int e = (i * T + t) * 8 - phase;
+    float f[8];
+    scaled<F32, ALIGNED>(f, v[i], col_scale, e, K);
+    store_codes<ALIGNED>(f, rs, codes + m * K, e, K);
   }
 }
 
 // Rows too long for registers: read twice (the second time mostly from L2).
-template <int VEC, bool F32>
+template <bool ALIGNED, bool F32>
 __global__ void __launch_bounds__(1024)
-    i8_quantize_long_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int64_t K,
+    i8_quantize_long_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int K,
                             int8_t *__restrict__ codes, float *__restrict__ scale) {
   __shared__ uint32_t slot[32];
   const int64_t m = blockIdx.x;
-  const void *row = F32 ? static_cast<const void *>(static_cast<const float *>(X) + m * K)
-                        : static_cast<const void *>(static_cast<const uint16_t *>(X) + m * K);
-  auto load = [&](float (&f)[VEC], int64_t k) {
-    load_row<VEC, F32>(f, row, k);
-    if (col_scale) {
-      float c[VEC];
-      load_row<VEC, true>(c, col_scale, k);
+  const void *row = row_at<F32>(X, m * K);
+  const int e0 = static_cast<int>(threadIdx.x) * 8 - (ALIGNED ? 0 : static_cast<int>((m * K) & 7));
+  float mx = 0.f;
+  for (int e = e0; e < K; e += 8192) {
+    Vec8<F32> v;
+    float f[8];
+    v.template load<ALIGNED>(row, e, K);
+    scaled<F32, ALIGNED>(f, v, col_scale, e, K);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) f[j] = __fmul_rn(f[j], c[j]);
-    }
-  };
-  uint32_t mx = 0;
-  for (int64_t k = static_cast<int64_t>(threadIdx.x) * VEC; k < K; k += static_cast<int64_t>(blockDim.x) * VEC) {
-    float f[VEC];
-    load(f, k);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) mx = max(mx, mag_bits(f[j]));
+    for (int j = 0; j < 8; ++j) mx = max_mag(mx, f[j]);
   }
-  const RowScale rs = row_scale(row_max<false>(mx, slot));
+  const RowScale rs = row_scale(row_max<false>(__float_as_uint(mx), slot));
   if (threadIdx.x == 0) scale[m] = rs.s;
-  for (int64_t k = static_cast<int64_t>(threadIdx.x) * VEC; k < K; k += static_cast<int64_t>(blockDim.x) * VEC) {
-    float f[VEC];
-    load(f, k);
-    store_codes<VEC>(f, rs, codes + m * K, k);
+  for (int e = e0; e < K; e += 8192) {
+    Vec8<F32> v;
+    float f[8];
+    v.template load<ALIGNED>(row, e, K);
+    scaled<F32, ALIGNED>(f, v, col_scale, e, K);
+    store_codes<ALIGNED>(f, rs, codes + m * K, e, K);
   }
 }
 
-template <int VEC>
+// Vectors of 16 (ALIGNED: K a multiple of 16) or of 8 codes over the whole matrix as one array; without
+// ALIGNED a vector may cross into the next rows.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
-    i8_dequantize_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int64_t M, int64_t K,
+    i8_dequantize_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int64_t M, int K,
                          uint16_t *__restrict__ out) {
-  const int64_t per_row = (K + VEC - 1) / VEC, total = M * per_row;
-  for (int64_t i = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
-    const int64_t m = i / per_row, k = (i - m * per_row) * VEC;
-    const float s = scale[m];
-    float f[VEC];
-    if constexpr (VEC == 8) {
-      const uint2 u = *reinterpret_cast<const uint2 *>(codes + m * K + k);
-      const uint32_t w[2] = {u.x, u.y};
+  constexpr int V = ALIGNED ? 16 : 8;
+  const int64_t total = M * K;
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * V; i < total;
+       i += static_cast<int64_t>(gridDim.x) * blockDim.x * V) {
+    int64_t m = i / K;
+    float s = scale[m];
+    if constexpr (ALIGNED) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(codes + i);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(w[j >> 2] >> (8 * (j & 3)))), s);
+      for (int h = 0; h < 2; ++h) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          f[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(w[2 * h + (j >> 2)] >> (8 * (j & 3)))), s);
+        store_vec<true, false>(f, out + i, 8 * h, 16);
+      }
     } else {
-      f[0] = __fmul_rn(static_cast<float>(codes[m * K + k]), s);
+      int64_t next = (m + 1) * K;   // the next row's first element
+      float f[8];
+      const int n = static_cast<int>(total - i < 8 ? total - i : 8);
+      uint32_t w[2] = {};
+      if (n == 8) {
+        const uint2 u = *reinterpret_cast<const uint2 *>(codes + i);
+        w[0] = u.x;
+        w[1] = u.y;
+      } else {
+        for (int j = 0; j < n; ++j) w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(codes[i + j])) << (8 * (j & 3));
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (i + j == next && j < n) {
+          s = scale[++m];
+          next += K;
+        }
+        f[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(w[j >> 2] >> (8 * (j & 3)))), s);
+      }
+      store_vec<false, false>(f, out + i, 0, n);
     }
-    store_row<VEC, false>(f, out + m * K, k);
   }
 }
-
-template <int VEC, int NV, bool WARP>
-cudaError_t quantize_nv(const void *X, bool f32, const float *cs, int64_t M, int64_t K, int8_t *codes, float *scale,
-                        int threads, cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(WARP ? (M + threads / 32 - 1) / (threads / 32) : M));
-  if (f32) i8_quantize_kernel<VEC, NV, WARP, true><<<grid, threads, 0, st>>>(X, cs, M, K, codes, scale);
-  else i8_quantize_kernel<VEC, NV, WARP, false><<<grid, threads, 0, st>>>(X, cs, M, K, codes, scale);
-  return cudaGetLastError();
-}
-
-template <int VEC>
-cudaError_t quantize_long(const void *X, bool f32, const float *cs, int64_t M, int64_t K, int8_t *codes, float *scale,
-                          cudaStream_t st) {
-  const dim3 grid(static_cast<unsigned>(M));
-  if (f32) i8_quantize_long_kernel<VEC, true><<<grid, 1024, 0, st>>>(X, cs, M, K, codes, scale);
-  else i8_quantize_long_kernel<VEC, false><<<grid, 1024, 0, st>>>(X, cs, M, K, codes, scale);
-  return cudaGetLastError();
-}
-
-int round32(int64_t t) { return static_cast<int>((t + 31) / 32 * 32); }
 
 }  // namespace
 
 cudaError_t launch_i8_quantize(const void *X, bool f32, int64_t M, int64_t K, const float *cs, int8_t *codes,
                                float *scale, cudaStream_t st) {
-  if (K % 8 == 0) {
-    const int64_t v = K / 8;
-    if (v <= 32) return quantize_nv<8, 1, true>(X, f32, cs, M, K, codes, scale, 128, st);
-    if (v <= 128) return quantize_nv<8, 4, true>(X, f32, cs, M, K, codes, scale, 128, st);
-    if (v <= 1024 && M <= 2 * device_sm_count())
-      return quantize_nv<8, 1, false>(X, f32, cs, M, K, codes, scale, round32(v), st);
-    if (v <= 2048) return quantize_nv<8, 2, false>(X, f32, cs, M, K, codes, scale, round32((v + 1) / 2), st);
-    if (v <= 4096) return quantize_nv<8, 4, false>(X, f32, cs, M, K, codes, scale, round32((v + 3) / 4), st);
-    return quantize_long<8>(X, f32, cs, M, K, codes, scale, st);
+  const RowPlan p = row_plan(M, K, device_sm_count(), 4);
+  const int k = static_cast<int>(K);
+  if (p.nv == 0) {
+    const unsigned grid = static_cast<unsigned>(M);
+    if (p.aligned && f32) i8_quantize_long_kernel<true, true><<<grid, 1024, 0, st>>>(X, cs, M, k, codes, scale);
+    else if (p.aligned) i8_quantize_long_kernel<true, false><<<grid, 1024, 0, st>>>(X, cs, M, k, codes, scale);
+    else if (f32) i8_quantize_long_kernel<false, true><<<grid, 1024, 0, st>>>(X, cs, M, k, codes, scale);
+    else i8_quantize_long_kernel<false, false><<<grid, 1024, 0, st>>>(X, cs, M, k, codes, scale);
+    return cudaGetLastError();
   }
-  if (K <= 128) return quantize_nv<1, 4, true>(X, f32, cs, M, K, codes, scale, 128, st);
-  if (K <= 8192) return quantize_nv<1, 8, false>(X, f32, cs, M, K, codes, scale, round32((K + 7) / 8), st);
-  if (K <= 32768) return quantize_nv<1, 32, false>(X, f32, cs, M, K, codes, scale, round32((K + 31) / 32), st);
-  return quantize_long<1>(X, f32, cs, M, K, codes, scale, st);
+  return dispatch_row(p, [&](auto nv, auto warp, auto aligned) {
+    if constexpr (nv.value == 2 && !warp.value) return cudaErrorInvalidValue;   // not a plan of this launch
+    else {
+      if (f32)
+        i8_quantize_kernel<nv.value, warp.value, aligned.value, true>
+            <<<row_grid(p, M), p.threads, 0, st>>>(X, cs, M, k, codes, scale);
+      else
+        i8_quantize_kernel<nv.value, warp.value, aligned.value, false>
+            <<<row_grid(p, M), p.threads, 0, st>>>(X, cs, M, k, codes, scale);
+      return cudaGetLastError();
+    }
+  });
 }
 
 cudaError_t launch_i8_dequantize(const int8_t *codes, const float *scale, int64_t M, int64_t K, uint16_t *out,
                                  cudaStream_t st) {
-  const int vec = K % 8 ? 1 : 8;
-  const int64_t blocks = (M * ((K + vec - 1) / vec) + 255) / 256, most = static_cast<int64_t>(device_sm_count()) * 8;
+  const int vec = K % 16 ? 8 : 16;
+  const int64_t blocks = (M * K + 256 * vec - 1) / (256 * vec), most = static_cast<int64_t>(device_sm_count()) * 16;
   const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  if (vec == 8) i8_dequantize_kernel<8><<<grid, 256, 0, st>>>(codes, scale, M, K, out);
-  else i8_dequantize_kernel<1><<<grid, 256, 0, st>>>(codes, scale, M, K, out);
+  if (vec == 16) i8_dequantize_kernel<true><<<grid, 256, 0, st>>>(codes, scale, M, static_cast<int>(K), out);
+  else i8_dequantize_kernel<false><<<grid, 256, 0, st>>>(codes, scale, M, static_cast<int>(K), out);
   return cudaGetLastError();
 }
 

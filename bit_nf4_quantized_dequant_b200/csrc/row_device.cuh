@@ -1,6 +1,15 @@
-// Device helpers of the row kernels (RMS norm, int8 row codec): vector loads
-// and stores of a row's elements as fp32, reductions over the threads of a
-// row, and the int8 code of a value.
+// Device helpers of the row kernels (RMS norm, int8 row codec): a row's elements
+// in vectors of eight, reductions over the threads of a row, the int8 code of a
+// value, and how threads share a row.
+//
+// All matrices of a call have the same shape [M, K], so their rows start at the
+// same phase (m K mod 8) of eight-element groups, and such a group is aligned
+// for a 16-byte access in each of them whatever K is (32 bytes of fp32, 16 of
+// bf16, 8 of codes). A row's vectors are those groups: vector i of a row of
+// phase p covers its elements 8 i - p .. 8 i - p + 7; where K is a multiple of 8
+// the phase is always 0, else a row's first and last vector may be partial and
+// are read and written element by element. Only the per-column vectors (weight,
+// column scales) are then out of phase, and come element by element from L1.
 #pragma once
 
 #include <cstdint>
@@ -10,57 +19,105 @@
 
 namespace qlora {
 
-// VEC consecutive elements (1 or 8) of a bf16 or fp32 row, as fp32. The
-// 8-element forms need the address aligned to 16 bytes.
-template <int VEC, bool F32>
-__device__ __forceinline__ void load_row(float (&f)[VEC], const void *row, int64_t i) {
-  if constexpr (F32) {
-    const float *p = static_cast<const float *>(row) + i;
-    if constexpr (VEC == 8) {
-      const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-      f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-      f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+__device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
+__device__ __forceinline__ float bf16_round(float x) { return __uint_as_float(pack_bf16x2(x, 0.f) << 16); }
+
+// Eight elements kept as they were loaded: four words of bf16, eight of fp32.
+template <bool F32>
+struct Vec8 {
+  static constexpr int kWords = F32 ? 8 : 4;
+  uint32_t w[kWords];
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int j = 0; j < kWords; ++j) w[j] = 0u;
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
+    if constexpr (F32) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
     } else {
-      f[0] = *p;
-    }
-  } else {
-    const uint16_t *p = static_cast<const uint16_t *>(row) + i;
-    if constexpr (VEC == 8) {
-      const uint4 u = *reinterpret_cast<const uint4 *>(p);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         f[2 * j] = __uint_as_float(w[j] << 16);
         f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
       }
-    } else {
-      f[0] = __uint_as_float(static_cast<uint32_t>(*p) << 16);
     }
   }
-}
-
-template <int VEC, bool F32>
-__device__ __forceinline__ void store_row(const float (&f)[VEC], void *row, int64_t i) {
-  if constexpr (F32) {
-    float *p = static_cast<float *>(row) + i;
-    if constexpr (VEC == 8) {
-      *reinterpret_cast<float4 *>(p) = make_float4(f[0], f[1], f[2], f[3]);
-      *reinterpret_cast<float4 *>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+  // Elements e .. e + 7 of a row of K; those outside it are zero.
+  template <bool ALIGNED>
+  __device__ __forceinline__ void load(const void *row, int e, int K) {
+    if (ALIGNED ? e < K : (e >= 0 && e + 8 <= K)) {
+      const uint4 *p = F32 ? reinterpret_cast<const uint4 *>(static_cast<const float *>(row) + e)
+                           : reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + e);
+#pragma unroll
+      for (int j = 0; j < kWords / 4; ++j) {
+        const uint4 u = p[j];
+        w[4 * j] = u.x; w[4 * j + 1] = u.y; w[4 * j + 2] = u.z; w[4 * j + 3] = u.w;
+      }
     } else {
-      *p = f[0];
+      zero();
+      if constexpr (!ALIGNED) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (e + j >= 0 && e + j < K) {
+            if constexpr (F32) w[j] = static_cast<const uint32_t *>(row)[e + j];
+            else w[j >> 1] |= static_cast<uint32_t>(static_cast<const uint16_t *>(row)[e + j]) << (16 * (j & 1));
+          }
+        }
+      }
     }
+  }
+};
+
+// Elements e .. e + 7 of a per-column vector (zero outside 0 .. K - 1).
+template <bool ALIGNED, bool F32>
+__device__ __forceinline__ void load_cols(float (&f)[8], const void *p, int e, int K) {
+  if constexpr (ALIGNED) {
+    Vec8<F32> v;
+    v.template load<true>(p, e, K);
+    v.get(f);
   } else {
-    uint16_t *p = static_cast<uint16_t *>(row) + i;
-    if constexpr (VEC == 8) {
-      *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]),
-                                                 pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
-    } else {
-      *p = static_cast<uint16_t>(pack_bf16x2(f[0], 0.f));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const bool in = e + j >= 0 && e + j < K;
+      if constexpr (F32) f[j] = in ? static_cast<const float *>(p)[e + j] : 0.f;
+      else f[j] = in ? bf16_to_f32(static_cast<const uint16_t *>(p)[e + j]) : 0.f;
     }
   }
 }
 
-__device__ __forceinline__ float bf16_round(float x) { return __uint_as_float(pack_bf16x2(x, 0.f) << 16); }
+template <bool ALIGNED, bool F32>
+__device__ __forceinline__ void store_vec(const float (&f)[8], void *row, int e, int K) {
+  if (ALIGNED ? e < K : (e >= 0 && e + 8 <= K)) {
+    if constexpr (F32) {
+      float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(row) + e);
+      p[0] = make_float4(f[0], f[1], f[2], f[3]);
+      p[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+      *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + e) =
+          make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+    }
+  } else if constexpr (!ALIGNED) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (e + j >= 0 && e + j < K) {
+        if constexpr (F32) static_cast<float *>(row)[e + j] = f[j];
+        else static_cast<uint16_t *>(row)[e + j] = static_cast<uint16_t>(pack_bf16x2(f[j], 0.f));
+      }
+    }
+  }
+}
+
+// A row's first element, by type.
+template <bool F32>
+__device__ __forceinline__ const void *row_at(const void *p, int64_t i) {
+  return F32 ? static_cast<const void *>(static_cast<const float *>(p) + i)
+             : static_cast<const void *>(static_cast<const uint16_t *>(p) + i);
+}
+template <bool F32>
+__device__ __forceinline__ void *row_at(void *p, int64_t i) {
+  return F32 ? static_cast<void *>(static_cast<float *>(p) + i) : static_cast<void *>(static_cast<uint16_t *>(p) + i);
+}
 
 // ---- reductions over the threads that share a row ---------------------------
 // One warp, or a whole block of up to 32 warps. `slot`: 32 words of shared
@@ -91,18 +148,22 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t *slot) {
   return __reduce_max_sync(0xffffffffu, lane < warps ? slot[lane] : 0u);
 }
 
-// |v| as an ordered integer: infinities and NaN sort above every finite value,
-// so one integer maximum finds the row's largest magnitude and whether the row
-// holds anything that is not finite.
-__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+// max(m, |v|) where a NaN stays: as bits, NaN and infinities sort above every
+// finite magnitude, so the row's maximum also says whether the row is finite.
+__device__ __forceinline__ float max_mag(float m, float v) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(m), "f"(fabsf(v)));
+  return r;
+}
 
-// The int8 code of a value, rint(fp32_rn(v / s)): v * (1 / s) is within
+// ---- int8 codes -------------------------------------------------------------
+// The code of a value, rint(fp32_rn(v / s)): v * (1 / s) is within
 // 3 * 127.5 * 2^-24 < 3e-5 of the quotient, so its rounding can differ only
-// next to a tie; there (about one value in five thousand) the division is
-// done. Adding 1.5 * 2^23 rounds to an integer, half to even, and leaves the
-// code in the low byte. |v| <= 127 s (1 + 2^-22) keeps the code within +-127
-// unless s is subnormal (rounded coarsely) or its reciprocal overflows: such
-// rows always divide, and clamp.
+// next to a tie; vectors with such a value (about one in six hundred) divide.
+// Adding 1.5 * 2^23 rounds to an integer, half to even, and leaves the code in
+// the low byte. |v| <= 127 s (1 + 2^-22) keeps the code within +-127 unless s is
+// subnormal (rounded coarsely) or its reciprocal overflows: such rows always
+// divide, and clamp.
 struct RowScale {
   float s, inv;
   bool zero, divide;
@@ -118,32 +179,82 @@ __device__ __forceinline__ RowScale row_scale(uint32_t max_bits) {
   r.inv = r.zero || r.divide ? 0.f : __frcp_rn(r.s);
   return r;
 }
-__device__ __forceinline__ uint32_t code_bits(float v, const RowScale &r) {
-  if (r.zero) return 0u;
-  if (r.divide) {
-    const float q = fminf(fmaxf(rintf(__fdiv_rn(v, r.s)), -127.f), 127.f);
-    return static_cast<uint32_t>(static_cast<int>(q));
-  }
-  float m = __fmaf_rn(v, r.inv, kRoundMagic);
-  const float d = __fmaf_rn(v, r.inv, -(m - kRoundMagic));
-  if (fabsf(fabsf(d) - 0.5f) < 1e-4f) m = __fadd_rn(__fdiv_rn(v, r.s), kRoundMagic);
-  return __float_as_uint(m);   // the code is the low byte
-}
 
-template <int VEC>
-__device__ __forceinline__ void store_codes(const float (&f)[VEC], const RowScale &r, int8_t *row, int64_t i) {
-  if constexpr (VEC == 8) {
-    uint32_t c[8];
+// Codes of elements e .. e + 7 of a row of K.
+template <bool ALIGNED>
+__device__ __forceinline__ void store_codes(const float (&f)[8], const RowScale &r, int8_t *row, int e, int K) {
+  uint32_t c[8];
+  float off = 0.f;   // the farthest of the values from its code
 #pragma unroll
-    for (int j = 0; j < 8; ++j) c[j] = code_bits(f[j], r);
+  for (int j = 0; j < 8; ++j) {
+    const float m = __fmaf_rn(f[j], r.inv, kRoundMagic);
+    off = fmaxf(off, fabsf(__fmaf_rn(f[j], r.inv, -(m - kRoundMagic))));
+    c[j] = __float_as_uint(m);
+  }
+  if (r.zero) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c[j] = 0u;
+  } else if (r.divide || off > 0.4999f) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      c[j] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(f[j], r.s)), -127.f), 127.f)));
+  }
+  if (ALIGNED ? e < K : (e >= 0 && e + 8 <= K)) {
     uint32_t w[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       w[j] = prmt(prmt(c[4 * j], c[4 * j + 1], 0x0040u), prmt(c[4 * j + 2], c[4 * j + 3], 0x0040u), 0x5410u);
-    *reinterpret_cast<uint2 *>(row + i) = make_uint2(w[0], w[1]);
-  } else {
-    row[i] = static_cast<int8_t>(code_bits(f[0], r) & 0xffu);
+    *reinterpret_cast<uint2 *>(row + e) = make_uint2(w[0], w[1]);
+  } else if constexpr (!ALIGNED) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      if (e + j >= 0 && e + j < K) row[e + j] = static_cast<int8_t>(c[j] & 0xffu);
   }
 }
+
+// ---- how threads share a row -------------------------------------------------
+// A warp or a block a row, `nv` vectors a thread (nv 0: as many passes as it
+// takes, for rows too long for registers). Few rows: one vector a thread, for
+// the latency. Many: `many` vectors, so that each SM holds several blocks, none
+// of which waits long at its barriers, with enough loads in flight.
+struct RowPlan {
+  int nv, threads;
+  bool warp, aligned;
+};
+inline RowPlan row_plan(int64_t M, int64_t K, int sms, int many) {
+  const int64_t v = K % 8 ? (K + 7) / 8 + 1 : K / 8;   // a row off phase may touch one vector more
+  auto per = [&](int nv) { return static_cast<int>((v + 32 * nv - 1) / (32 * nv) * 32); };
+  const bool aligned = K % 8 == 0;
+  if (v <= 32) return {1, 128, true, aligned};
+  if (v <= 64) return {2, 128, true, aligned};
+  if (v <= 1024 && M <= 2 * sms) return {1, per(1), false, aligned};
+  if (v <= 128) return {4, 128, true, aligned};
+  if (many == 2 && v <= 1024) return {2, per(2), false, aligned};
+  if (v <= 2048) return {4, per(4), false, aligned};
+  if (v <= 4097) return {8, per(8), false, aligned};
+  return {0, 1024, false, aligned};
+}
+
+// Numbers as types, and a call of go(nv, warp, aligned) with the plan's.
+template <int V>
+struct Num {
+  static constexpr int value = V;
+};
+template <class F>
+auto dispatch_row(const RowPlan &p, F go) {
+  auto with = [&](auto aligned) {
+    if (p.warp) return p.nv == 1 ? go(Num<1>{}, Num<1>{}, aligned) : p.nv == 2 ? go(Num<2>{}, Num<1>{}, aligned) : go(Num<4>{}, Num<1>{}, aligned);
+    return p.nv == 1   ? go(Num<1>{}, Num<0>{}, aligned)
+           : p.nv == 2 ? go(Num<2>{}, Num<0>{}, aligned)
+           : p.nv == 4 ? go(Num<4>{}, Num<0>{}, aligned)
+                       : go(Num<8>{}, Num<0>{}, aligned);
+  };
+  return p.aligned ? with(Num<1>{}) : with(Num<0>{});
+}
+inline unsigned row_grid(const RowPlan &p, int64_t M) {
+  return static_cast<unsigned>(p.warp ? (M + p.threads / 32 - 1) / (p.threads / 32) : M);
+}
+// The most threads a plan gives a block of nv vectors a thread.
+constexpr int row_threads(int nv, bool warp) { return warp ? 128 : (nv == 1 ? 1024 : (nv == 8 ? 544 : 512)); }
 
 }  // namespace qlora
