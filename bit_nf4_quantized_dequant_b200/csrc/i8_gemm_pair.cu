@@ -2,10 +2,10 @@
 // the SMs.
 //
 // A pair (cta_group::2, a cluster of two) computes a tile of 256 tokens (UMMA
-// M, 128 a CTA) by 256 features (UMMA N, each CTA loads 128 of them), so a step
-// of 128 codes needs 32 KB of shared memory a CTA for 512 tensor cycles. The
-// int32 accumulator takes 256 TMEM columns and is double-buffered: the epilogue
-// of one tile runs under the main loop of the next.
+// M, 128 a CTA) by up to 256 features (UMMA N, each CTA loads half of them), so
+// a step of 128 codes needs 32 KB of shared memory a CTA for 512 tensor cycles.
+// The int32 accumulator takes 256 TMEM columns and is double-buffered: the
+// epilogue of one tile runs under the main loop of the next.
 //
 // The epilogue reads TMEM in the fragment layout of the warp-level MMA
 // (16x256b: a thread holds two neighbouring features of rows T / 4 and
@@ -23,6 +23,8 @@
 // Warps (384 threads): 0 TMA producer, 1 MMA issuer and TMEM owner, 2 adapter
 // producer, 4-11 epilogue (TMEM lane quadrant warp % 4, half of the columns
 // each).
+#include <climits>
+
 #include "i8_gemm.cuh"
 
 namespace qlora {
@@ -33,11 +35,10 @@ bool encode_2d(CUtensorMap *map, CUtensorMapDataType dtype, const void *base, ui
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kTile = 256;                                 // tokens and features per pair tile
+constexpr int kTile = 256;                                 // tokens per pair tile, and the most features
 constexpr uint32_t kBoxBytes = 128 * kI8Step;              // 16 KiB: 128 tokens, or 128 features, of a step
-constexpr uint32_t kSlotBytes = 2 * kBoxBytes;
-constexpr int kMaxStages = 6;
-constexpr uint32_t kOutBytes = 16 * 128;                   // 16 tokens x 64 features bf16, per epilogue warp
+constexpr int kMaxStages = 9;
+constexpr uint32_t kOutBytes = 32 * 64;                    // 32 tokens x 32 features bf16, per epilogue warp
 constexpr int kEpiWarps = 8;
 
 struct PairParams {
@@ -45,6 +46,7 @@ struct PairParams {
   int32_t *status;
   int64_t M, F;
   int r_pad, stages;   // adapter ranks in shared memory (0, 16, 32 or 64), ring depth
+  int feat;            // features per pair tile, a multiple of 32
   int nk, feat_tiles, tok_tiles;
 };
 
@@ -56,20 +58,22 @@ struct PairBars {
   int abort_flag;
 };
 __host__ __device__ inline uint32_t lora_bytes(int r_pad) { return 128u * static_cast<uint32_t>(r_pad) * 2u; }
-__host__ __device__ inline uint32_t bars_offset(int stages, int r_pad) {
-  return static_cast<uint32_t>(stages) * kSlotBytes + kEpiWarps * kOutBytes + 2u * lora_bytes(r_pad);
+// A CTA's 128 tokens and its half of the features (DX: 128, of which it uses
+// the first feat / 2) of a step.
+__host__ __device__ inline uint32_t slot_bytes(bool dx, int feat) {
+  return kBoxBytes + (dx ? kBoxBytes : static_cast<uint32_t>(feat / 2) * kI8Step);
+}
+__host__ __device__ inline uint32_t bars_offset(uint32_t slot, int stages, int r_pad) {
+  return static_cast<uint32_t>(stages) * slot + kEpiWarps * kOutBytes + 2u * lora_bytes(r_pad);
 }
 
-// The reverse of tmem_ld_frag64.
-__device__ __forceinline__ void tmem_st_frag64(uint32_t taddr, const uint32_t (&r)[32]) {
+// The reverse of tmem_ld_frag32.
+__device__ __forceinline__ void tmem_st_frag32(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.16x256b.x8.b32 [%32], "
-      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31};" ::"r"(r[0]),
+      "tcgen05.st.sync.aligned.16x256b.x4.b32 [%16], "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]),
       "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
-      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]),
-      "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-      "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(taddr)
+      "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
@@ -87,9 +91,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tm_lora_act, const PairParams p) {
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint8_t *out_stage = ring + static_cast<uint32_t>(p.stages) * kSlotBytes;
+  const uint32_t slot_sz = slot_bytes(kDx, p.feat), half_feat = static_cast<uint32_t>(p.feat) / 2u;
+  uint8_t *out_stage = ring + static_cast<uint32_t>(p.stages) * slot_sz;
   uint8_t *lora_a = out_stage + kEpiWarps * kOutBytes, *lora_b = lora_a + lora_bytes(p.r_pad);
-  PairBars &sm = *reinterpret_cast<PairBars *>(ring + bars_offset(p.stages, p.r_pad));
+  PairBars &sm = *reinterpret_cast<PairBars *>(ring + bars_offset(slot_sz, p.stages, p.r_pad));
   volatile int *abort_flag = &sm.abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
@@ -98,7 +103,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int first = static_cast<int>(blockIdx.x >> 1), stride = static_cast<int>(gridDim.x >> 1);
   // tile -> (tokens, features): tokens fastest, so that the pairs at work share few weight tiles
   auto tok0 = [&](int tile) { return (tile % p.tok_tiles) * kTile; };
-  auto feat0 = [&](int tile) { return (tile / p.tok_tiles) * kTile; };
+  auto feat0 = [&](int tile) { return (tile / p.tok_tiles) * p.feat; };
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
@@ -141,15 +146,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t ph = 0, landed = 0, par = 0;
       bool ok = true;
       for (int tile = first; tile < ntiles && ok; tile += stride) {
-        const int t0 = tok0(tile) + static_cast<int>(rank) * 128, f0 = feat0(tile) + static_cast<int>(rank) * 128;
+        const int t0 = tok0(tile) + static_cast<int>(rank) * 128, f0 = feat0(tile) + static_cast<int>(rank * half_feat);
         for (int s = 0; s < p.nk; ++s) {
           if (!mbar_wait(&sm.empty[slot], ph ^ 1u, abort_flag, p.status)) {
             ok = false;
             break;
           }
-          if (leader) mbar_arrive_expect_tx(&sm.full[slot], 2 * kSlotBytes);
+          if (leader) mbar_arrive_expect_tx(&sm.full[slot], 2 * slot_sz);
           const uint32_t bar = mapa_shared(smem_u32(&sm.full[slot]), 0u);
-          uint8_t *x = ring + static_cast<uint32_t>(slot) * kSlotBytes;
+          uint8_t *x = ring + static_cast<uint32_t>(slot) * slot_sz;
           tma_load_2d_pair(x, &tm_act, bar, s * kI8Step, t0);
           if (!kDx) tma_load_2d_pair(x + kBoxBytes, &tm_w, bar, s * kI8Step, f0);
           else      tma_load_2d_pair(x + kBoxBytes, &tm_w, bar, f0, s * kI8Step);
@@ -170,14 +175,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (kLora && elect_one()) {
       bool issued = false, ok = true;
       uint32_t ph = 0;
-      const uint32_t bar = mapa_shared(smem_u32(&sm.loraf), 0u);
+      const uint32_t bar = mapa_shared(smem_u32(&sm.loraf), 0u), span = 2u * static_cast<uint32_t>(p.r_pad);
       for (int tile = first; tile < ntiles; tile += stride, ph ^= 1u) {
         if (!mbar_wait(&sm.lorae, ph ^ 1u, abort_flag, p.status)) {
           ok = false;
           break;
         }
-        const int t0 = tok0(tile) + static_cast<int>(rank) * 128, f0 = feat0(tile) + static_cast<int>(rank) * 128;
-        if (leader) mbar_arrive_expect_tx(&sm.loraf, 4 * lora_bytes(p.r_pad));
+        const int t0 = tok0(tile) + static_cast<int>(rank) * 128, f0 = feat0(tile) + static_cast<int>(rank * half_feat);
+        if (leader) mbar_arrive_expect_tx(&sm.loraf, 2 * (lora_bytes(p.r_pad) + (kDx ? 128u : half_feat) * span));
         tma_load_2d_pair(lora_a, &tm_lora_act, bar, 0, t0);
         if (!kDx) {
           tma_load_2d_pair(lora_b, &tm_lora_w, bar, 0, f0);
@@ -192,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 1) {
     // ---------------- MMA issuer (even CTA) ----------------
     if (leader && elect_one()) {
-      constexpr uint32_t idesc = idesc_i8(256, kTile, false, kDx);
+      const uint32_t idesc = idesc_i8(256, static_cast<uint32_t>(p.feat), false, kDx);
       const uint64_t a0 = smem_desc(smem_u32(ring), 16u, 1024u, kLayoutSW128);
       const uint64_t b0 = smem_desc(smem_u32(ring) + kBoxBytes, kDx ? kBoxBytes : 16u, 1024u, kLayoutSW128);
       // a step of 32 codes: +32 bytes along a K-major row, or 32 rows of 128 bytes (MN-major)
@@ -203,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto add_lora = [&](int i) -> bool {
         if (!mbar_wait(&sm.loraf, static_cast<uint32_t>(i) & 1u, abort_flag, p.status)) return false;
         tc_fence_after();
-        constexpr uint32_t lidesc = idesc_bf16(256, kTile, false, kDx);
+        const uint32_t lidesc = idesc_bf16(256, static_cast<uint32_t>(p.feat), false, kDx);
         for (uint32_t j = 0; j < static_cast<uint32_t>(p.r_pad) / 16u; ++j) {
           const uint64_t ad = smem_desc(smem_u32(lora_a) + 32u * j, 16u, 8u * span, lsw);
           const uint64_t bd = kDx ? smem_desc(smem_u32(lora_b) + 2048u * j, 64u * span, 1024u, kLayoutSW128)
@@ -237,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          const uint64_t off = (static_cast<uint32_t>(slot) * kSlotBytes) >> 4;
+          const uint64_t off = (static_cast<uint32_t>(slot) * slot_sz) >> 4;
 #pragma unroll
           for (uint32_t j = 0; j < kI8Step / 32; ++j)
             umma_i8_pair(d, a0 + off + j * 2u, b0 + off + j * b_step, idesc, s || j);
@@ -261,18 +266,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 4) {
     // ---------------- epilogue ----------------
-    const int quad = warp & 3, half = (warp - 4) >> 2;   // 32 tokens, 128 features of the CTA's 128 x 256
+    const int quad = warp & 3, half = (warp - 4) >> 2;   // 32 tokens; every other chunk of 32 features
     uint8_t *stage = out_stage + static_cast<uint32_t>(warp - 4) * kOutBytes;
     const int g = lane >> 2, q2 = (lane & 3) * 2;        // fragment row and column pair
-    const uint32_t st_row = lane & 15, st_chunk = lane >> 4;   // this lane's stmatrix row and first 16-byte chunk
-    const uint32_t st_addr = smem_u32(stage) + st_row * 128u;
-    const uint32_t t_warp = tmem + (static_cast<uint32_t>(quad * 32) << 16) + half * 128;
+    const int chunks = p.feat / 32;
+    const uint32_t t_warp = tmem + (static_cast<uint32_t>(quad * 32) << 16);
+    // this lane's stmatrix address for tokens h * 16 .. + 15: row of 64 bytes, swizzled 16-byte chunks
+    auto st_addr = [&](int h, int j) -> uint32_t {
+      const uint32_t row = static_cast<uint32_t>(h * 16 + (lane & 15)), chunk = static_cast<uint32_t>(j + (lane >> 4));
+      return smem_u32(stage) + swizzle_off(row * 64u + chunk * 16u, 64u);
+    };
     int n = 0;
     bool ok = true;
     for (int tile = first; tile < ntiles && ok; tile += stride, ++n) {
       const int buf = n & 1;
       const int64_t m0 = static_cast<int64_t>(tok0(tile)) + rank * 128 + quad * 32;
-      const int64_t f0 = static_cast<int64_t>(feat0(tile)) + half * 128;
+      const int64_t f0 = static_cast<int64_t>(feat0(tile));
       const uint32_t t_acc = t_warp + buf * kTile;
       float sx[4];   // tokens g, g + 8, g + 16, g + 24
 #pragma unroll
@@ -282,10 +291,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc_fence_after();
-      // sums to scaled fp32, in the thread's 2 x 16 values of 64 features by 16 tokens (h: which 16)
-      auto scale = [&](uint32_t (&v)[32], const float2 (&sw)[8], int h) {
+      // sums to scaled fp32: the thread's 2 x 8 values of 32 features by 16 tokens (h: which 16)
+      auto scale = [&](uint32_t (&v)[16], const float2 (&sw)[4], int h) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             float y = static_cast<float>(static_cast<int>(v[4 * j + e])) * (h ? sx[2 + (e >> 1)] : sx[e >> 1]);
@@ -293,28 +302,28 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[4 * j + e] = __float_as_uint(y);
           }
       };
-      auto load_sw = [&](float2 (&sw)[8], int64_t fc) {
+      auto load_sw = [&](float2 (&sw)[4], int64_t fc) {
         if constexpr (!kDx) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
+          for (int j = 0; j < 4; ++j) {
             const int64_t f = fc + j * 8 + q2;
             sw[j] = f < p.F ? __ldg(reinterpret_cast<const float2 *>(p.w_scale + f)) : make_float2(0.f, 0.f);
           }
         }
       };
       if constexpr (kLora) {
-#pragma unroll 1
-        for (int ch = 0; ch < 2; ++ch) {
-          float2 sw[8];
-          uint32_t v[2][32];
-          tmem_ld_frag64(t_acc + ch * 64, v[0]);
-          tmem_ld_frag64(t_acc + ch * 64 + (16u << 16), v[1]);
-          load_sw(sw, f0 + ch * 64);
+#pragma unroll 2
+        for (int c = half; c < chunks; c += 2) {
+          float2 sw[4];
+          uint32_t v[2][16];
+          tmem_ld_frag32(t_acc + c * 32, v[0]);
+          tmem_ld_frag32(t_acc + c * 32 + (16u << 16), v[1]);
+          load_sw(sw, f0 + c * 32);
           tmem_ld_wait();
           scale(v[0], sw, 0);
-          tmem_st_frag64(t_acc + ch * 64, v[0]);
+          tmem_st_frag32(t_acc + c * 32, v[0]);
           scale(v[1], sw, 1);
-          tmem_st_frag64(t_acc + ch * 64 + (16u << 16), v[1]);
+          tmem_st_frag32(t_acc + c * 32 + (16u << 16), v[1]);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -326,38 +335,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
       }
-#pragma unroll 1
-      for (int ch = 0; ch < 2; ++ch) {
-        const int64_t fc = f0 + ch * 64;
-        float2 sw[8];
-        uint32_t v[2][32];
-        tmem_ld_frag64(t_acc + ch * 64, v[0]);
-        tmem_ld_frag64(t_acc + ch * 64 + (16u << 16), v[1]);
+#pragma unroll 2
+      for (int c = half; c < chunks; c += 2) {
+        const int64_t fc = f0 + c * 32;
+        float2 sw[4];
+        uint32_t v[2][16];
+        tmem_ld_frag32(t_acc + c * 32, v[0]);
+        tmem_ld_frag32(t_acc + c * 32 + (16u << 16), v[1]);
         if constexpr (!kLora) load_sw(sw, fc);
         tmem_ld_wait();
-        if (ch == 1) {   // the accumulator is in registers: the next tile but one may have it
+        if (c + 2 >= chunks) {   // this warp's part is in registers: the next tile but one may have the accumulator
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive_cluster(mapa_shared(smem_u32(&sm.acce[buf]), 0u));
         }
+        // the staging tile is free again once the previous store has read it
+        if (lane == 0) bulk_wait_group_read<0>();
+        __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           if constexpr (!kLora) scale(v[h], sw, h);
-          // the staging tile is free again once the previous store has read it
-          if (lane == 0) bulk_wait_group_read<0>();
-          __syncwarp();
+          auto pack = [&](int i) { return pack_bf16x2(__uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1])); };
 #pragma unroll
-          for (int j = 0; j < 8; j += 2) {
-            auto pack = [&](int i) { return pack_bf16x2(__uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1])); };
-            stmatrix_x4(st_addr + (((j + st_chunk) ^ (st_row & 7u)) << 4), pack(4 * j), pack(4 * j + 2), pack(4 * j + 4),
-                        pack(4 * j + 6));
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0 && m0 + h * 16 < p.M && fc < p.F) {
-            tma_store_2d(&tm_out, stage, static_cast<int32_t>(fc), static_cast<int32_t>(m0 + h * 16));
-            bulk_commit_group();
-          }
+          for (int j = 0; j < 4; j += 2)
+            stmatrix_x4(st_addr(h, j), pack(4 * j), pack(4 * j + 2), pack(4 * j + 4), pack(4 * j + 6));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && m0 < p.M && fc < p.F) {
+          tma_store_2d(&tm_out, stage, static_cast<int32_t>(fc), static_cast<int32_t>(m0));
+          bulk_commit_group();
         }
       }
     }
@@ -387,16 +394,35 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
   p.M = a.M;
   p.F = a.F;
   p.r_pad = a.r == 0 ? 0 : (a.r <= 16 ? 16 : (a.r <= 32 ? 32 : 64));
-  p.stages = p.r_pad <= 32 ? 6 : 5;   // what 227 KB hold beside the adapter's tiles
   p.nk = static_cast<int>((a.C + kI8Step - 1) / kI8Step);
-  p.feat_tiles = static_cast<int>((a.F + kTile - 1) / kTile);
   p.tok_tiles = static_cast<int>((a.M + kTile - 1) / kTile);
+  // Features per tile (FWD): the least waves times the bytes of a step, so that
+  // a launch of less than one wave spreads over the SMs. DX loads 128 features a
+  // CTA in any case (a swizzled row of the weight box): 256.
+  const int64_t pairs = device_sm_count() / 2;
+  p.feat = kTile;
+  if (!a.dx) {
+    int64_t best = LLONG_MAX;
+    for (int feat = kTile; feat >= 96; feat -= 32) {
+      const int64_t tiles = (a.F + feat - 1) / feat * p.tok_tiles, cost = (tiles + pairs - 1) / pairs * (kTile + feat);
+      if (cost < best) {
+        best = cost;
+        p.feat = feat;
+      }
+    }
+  }
+  p.feat_tiles = static_cast<int>((a.F + p.feat - 1) / p.feat);
+  const uint32_t slot = slot_bytes(a.dx, p.feat);
+  // what 227 KB hold beside the staging, the adapter's tiles, the barriers and the alignment
+  p.stages = static_cast<int>((232448u - 1024u - 512u - bars_offset(slot, 0, p.r_pad)) / slot);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
 
   CUtensorMap tm_w, tm_act, tm_out, tm_lora_w, tm_lora_act;
   const uint64_t wrow = static_cast<uint64_t>(a.dx ? a.F : a.C), wrows = static_cast<uint64_t>(a.dx ? a.C : a.F);
-  bool ok = encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, wrow, wrows, wrow, 128, 128, CU_TENSOR_MAP_SWIZZLE_128B);
+  bool ok = encode_2d(&tm_w, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.w, wrow, wrows, wrow, 128,
+                      a.dx ? 128 : p.feat / 2, CU_TENSOR_MAP_SWIZZLE_128B);
   ok &= encode_2d(&tm_act, CU_TENSOR_MAP_DATA_TYPE_UINT8, a.act, a.C, a.M, a.C, kI8Step, 128, CU_TENSOR_MAP_SWIZZLE_128B);
-  ok &= encode_2d(&tm_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.F, a.M, a.F * 2, 64, 16, CU_TENSOR_MAP_SWIZZLE_128B);
+  ok &= encode_2d(&tm_out, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.out, a.F, a.M, a.F * 2, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B);
   tm_lora_w = tm_lora_act = tm_out;
   if (a.r) {
     const CUtensorMapSwizzle sw = p.r_pad == 16   ? CU_TENSOR_MAP_SWIZZLE_32B
@@ -405,14 +431,16 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
     ok &= encode_2d(&tm_lora_act, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_act, a.r, a.M, a.r * 2, p.r_pad, 128, sw);
     ok &= a.dx ? encode_2d(&tm_lora_w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_w, a.F, a.r, a.F * 2, 64, p.r_pad,
                            CU_TENSOR_MAP_SWIZZLE_128B)
-               : encode_2d(&tm_lora_w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_w, a.r, a.F, a.r * 2, p.r_pad, 128, sw);
+               : encode_2d(&tm_lora_w, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, a.lora_w, a.r, a.F, a.r * 2, p.r_pad,
+                           p.feat / 2, sw);
   }
   if (!ok) return cudaErrorInvalidValue;
   const void *fn = a.dx ? pair_fn<true>(a.r != 0) : pair_fn<false>(a.r != 0);
-  const size_t smem = 1024 + bars_offset(p.stages, p.r_pad) + sizeof(PairBars);
+  static_assert(sizeof(PairBars) <= 512, "room kept for the barriers");
+  const size_t smem = 1024 + bars_offset(slot, p.stages, p.r_pad) + sizeof(PairBars);
   cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  const int64_t tiles = static_cast<int64_t>(p.feat_tiles) * p.tok_tiles, pairs = device_sm_count() / 2;
+  const int64_t tiles = static_cast<int64_t>(p.feat_tiles) * p.tok_tiles;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
   cfg.blockDim = dim3(kThreads);

@@ -16,6 +16,8 @@
 // sum, scales, adapter (mma.m16n8k16), bf16, 32-byte row segments stored.
 //
 // Warps: 0 TMA producer, 1 MMA issuer and TMEM owner; all eight finish.
+#include <atomic>
+
 #include "i8_gemm.cuh"
 
 namespace qlora {
@@ -299,6 +301,37 @@ const void *split_fn(int steps) {
 
 }  // namespace
 
+// Clusters of `split` CTAs that the current device holds at a time, one CTA a
+// SM: what the driver says, asked once a device and size.
+static int resident_clusters(int split) {
+  static std::atomic<int> known[64][kMaxSplit + 1];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  int n = known[dev][split].load(std::memory_order_relaxed);
+  if (n == 0) {
+    const void *fn = reinterpret_cast<const void *>(i8_split_kernel<false, 0>);
+    const int smem = 200 * 1024;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(split * device_sm_count()));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
+      cudaGetLastError();   // no answer is no reason to fail: no split
+      n = 1;
+    }
+    known[dev][split].store(n, std::memory_order_relaxed);
+  }
+  return n;
+}
+
 cudaError_t launch_i8_split(const I8GemmArgs &a, cudaStream_t st) {
   SplitParams p{};
   p.act_scale = a.act_scale;
@@ -317,10 +350,9 @@ cudaError_t launch_i8_split(const I8GemmArgs &a, cudaStream_t st) {
   // As many CTAs as there are SMs, each with about four steps or more. Measured
   // with one token of 4096 x 4096 (32 tiles of 32 steps): 4 ways 6.3 us, 3 ways
   // 6.7, 2 ways 7.2, 8 ways (two CTAs a SM) 7.2; 1024 x 4096: 8 ways 5.1, 4 ways 5.9.
-  // A cluster stays inside one of the eight GPCs, so a GPC's 18 SMs hold 18 / split of them.
-  const int gpc_sms = device_sm_count() / 8;
+  // A cluster stays inside one GPC, which leaves some SMs out: see resident_clusters.
   p.split = (p.nk + 3) / 4 < kMaxSplit ? (p.nk + 3) / 4 : kMaxSplit;
-  while (p.split > 1 && tiles > 8 * (gpc_sms / p.split)) --p.split;
+  while (p.split > 1 && tiles > resident_clusters(p.split)) --p.split;
   const int per_cta = (p.nk + p.split - 1) / p.split;
   // two CTAs a SM where there are more than SMs, else one with a deeper ring
   const uint32_t room = (tiles * p.split > device_sm_count() ? 108u : 200u) * 1024u;
