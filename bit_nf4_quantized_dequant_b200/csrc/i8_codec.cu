@@ -13,13 +13,13 @@ namespace qlora {
 namespace {
 
 template <bool F32, bool ALIGNED>
-__device__ __forceinline__ void scaled(float (&f)[8], const Vec8<F32> &v, const float *col_scale, int e, int K) {
+__device__ __forceinline__ void scaled(f2 (&f)[4], const Vec8<F32> &v, const float *col_scale, int e, int K) {
   v.get(f);
   if (col_scale) {
-    float c[8];
+    f2 c[4];
     load_cols<ALIGNED, true>(c, col_scale, e, K);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = __fmul_rn(f[j], c[j]);
+    for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], c[j]);
   }
 }
 
@@ -41,17 +41,17 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 1 || 
   float mx = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float f[8];
+    f2 f[4];
     scaled<F32, ALIGNED>(f, v[i], col_scale, (i * T + t) * 8 - phase, K);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mx = max_mag(mx, f[j]);
+    for (int j = 0; j < 4; ++j) mx = max_mag(max_mag(mx, lo2(f[j])), hi2(f[j]));
   }
   const RowScale rs = row_scale(row_max<WARP>(__float_as_uint(mx), slot));
   if (t == 0) scale[m] = rs.s;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = (i * T + t) * 8 - phase;
-    float f[8];
+    f2 f[4];
     scaled<F32, ALIGNED>(f, v[i], col_scale, e, K);
     store_codes<ALIGNED>(f, rs, codes + m * K, e, K);
   }
@@ -69,69 +69,84 @@ __global__ void __launch_bounds__(1024)
   float mx = 0.f;
   for (int e = e0; e < K; e += 8192) {
     Vec8<F32> v;
-    float f[8];
+    f2 f[4];
     v.template load<ALIGNED>(row, e, K);
     scaled<F32, ALIGNED>(f, v, col_scale, e, K);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mx = max_mag(mx, f[j]);
+    for (int j = 0; j < 4; ++j) mx = max_mag(max_mag(mx, lo2(f[j])), hi2(f[j]));
   }
   const RowScale rs = row_scale(row_max<false>(__float_as_uint(mx), slot));
   if (threadIdx.x == 0) scale[m] = rs.s;
   for (int e = e0; e < K; e += 8192) {
     Vec8<F32> v;
-    float f[8];
+    f2 f[4];
     v.template load<ALIGNED>(row, e, K);
     scaled<F32, ALIGNED>(f, v, col_scale, e, K);
     store_codes<ALIGNED>(f, rs, codes + m * K, e, K);
   }
 }
 
-// Vectors of 16 (ALIGNED: K a multiple of 16) or of 8 codes over the whole matrix as one array; without
-// ALIGNED a vector may cross into the next rows.
-template <bool ALIGNED>
+// K a multiple of 16: a block takes 512 vectors of 16 codes of one row.
+__global__ void __launch_bounds__(256)
+    i8_dequantize_rows_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int K, int blocks_a_row,
+                              uint16_t *__restrict__ out) {
+  const uint32_t m = blockIdx.x / static_cast<uint32_t>(blocks_a_row), b = blockIdx.x - m * static_cast<uint32_t>(blocks_a_row);
+  const float s = scale[m];
+  const int64_t base = static_cast<int64_t>(m) * K;
+  const int k0 = static_cast<int>(b) * 8192 + static_cast<int>(threadIdx.x) * 16;
+  uint4 u[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    if (k0 + i * 4096 < K) u[i] = *reinterpret_cast<const uint4 *>(codes + base + k0 + i * 4096);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (k0 + i * 4096 < K) {
+      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        f2 f[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          auto code = [&](int b) { return static_cast<float>(static_cast<int8_t>(w[2 * h + (b >> 2)] >> (8 * (b & 3)))); };
+          f[j] = mul2(pair2(code(2 * j), code(2 * j + 1)), both(s));
+        }
+        store_vec<true, false>(f, out + base, k0 + i * 4096 + 8 * h, K);
+      }
+    }
+  }
+}
+
+// Any K: vectors of 8 codes over the whole matrix as one array; a vector may
+// cross into the next rows.
 __global__ void __launch_bounds__(256)
     i8_dequantize_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int64_t M, int K,
                          uint16_t *__restrict__ out) {
-  constexpr int V = ALIGNED ? 16 : 8;
-  const int64_t total = M * K;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) * V; i < total;
-       i += static_cast<int64_t>(gridDim.x) * blockDim.x * V) {
-    int64_t m = i / K;
-    float s = scale[m];
-    if constexpr (ALIGNED) {
-      const uint4 u = *reinterpret_cast<const uint4 *>(codes + i);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float f[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          f[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(w[2 * h + (j >> 2)] >> (8 * (j & 3)))), s);
-        store_vec<true, false>(f, out + i, 8 * h, 16);
-      }
-    } else {
-      int64_t next = (m + 1) * K;   // the next row's first element
-      float f[8];
-      const int n = static_cast<int>(total - i < 8 ? total - i : 8);
-      uint32_t w[2] = {};
-      if (n == 8) {
-        const uint2 u = *reinterpret_cast<const uint2 *>(codes + i);
-        w[0] = u.x;
-        w[1] = u.y;
-      } else {
-        for (int j = 0; j < n; ++j) w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(codes[i + j])) << (8 * (j & 3));
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (i + j == next && j < n) {
-          s = scale[++m];
-          next += K;
-        }
-        f[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(w[j >> 2] >> (8 * (j & 3)))), s);
-      }
-      store_vec<false, false>(f, out + i, 0, n);
-    }
+  const int64_t total = M * K, i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
+  if (i >= total) return;
+  // the block's first row by one division, this vector's from there
+  const int64_t m0 = static_cast<int64_t>(blockIdx.x) * 2048 / K;
+  const uint32_t in = static_cast<uint32_t>(i - m0 * K);   // below K + 2048
+  int64_t m = m0 + in / static_cast<uint32_t>(K), next = (m + 1) * K;   // next: the next row's first element
+  float s = scale[m], f[8];
+  const int n = static_cast<int>(total - i < 8 ? total - i : 8);
+  uint32_t w[2] = {};
+  if (n == 8) {
+    const uint2 u = *reinterpret_cast<const uint2 *>(codes + i);
+    w[0] = u.x;
+    w[1] = u.y;
+  } else {
+    for (int j = 0; j < n; ++j) w[j >> 2] |= static_cast<uint32_t>(static_cast<uint8_t>(codes[i + j])) << (8 * (j & 3));
   }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    if (i + j == next && j < n) {
+      s = scale[++m];
+      next += K;
+    }
+    f[j] = __fmul_rn(static_cast<float>(static_cast<int8_t>(w[j >> 2] >> (8 * (j & 3)))), s);
+  }
+  const f2 v[4] = {pair2(f[0], f[1]), pair2(f[2], f[3]), pair2(f[4], f[5]), pair2(f[6], f[7])};
+  store_vec<false, false>(v, out + i, 0, n);
 }
 
 }  // namespace
@@ -164,11 +179,13 @@ cudaError_t launch_i8_quantize(const void *X, bool f32, int64_t M, int64_t K, co
 
 cudaError_t launch_i8_dequantize(const int8_t *codes, const float *scale, int64_t M, int64_t K, uint16_t *out,
                                  cudaStream_t st) {
-  const int vec = K % 16 ? 8 : 16;
-  const int64_t blocks = (M * K + 256 * vec - 1) / (256 * vec), most = static_cast<int64_t>(device_sm_count()) * 16;
-  const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
-  if (vec == 16) i8_dequantize_kernel<true><<<grid, 256, 0, st>>>(codes, scale, M, static_cast<int>(K), out);
-  else i8_dequantize_kernel<false><<<grid, 256, 0, st>>>(codes, scale, M, static_cast<int>(K), out);
+  const int64_t a_row = (K + 8191) / 8192;
+  if (K % 16 == 0 && M * a_row < (int64_t(1) << 31))
+    i8_dequantize_rows_kernel<<<static_cast<unsigned>(M * a_row), 256, 0, st>>>(codes, scale, static_cast<int>(K),
+                                                                                static_cast<int>(a_row), out);
+  else
+    i8_dequantize_kernel<<<static_cast<unsigned>((M * K + 2047) / 2048), 256, 0, st>>>(codes, scale, M,
+                                                                                       static_cast<int>(K), out);
   return cudaGetLastError();
 }
 

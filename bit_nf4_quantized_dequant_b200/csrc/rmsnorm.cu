@@ -17,7 +17,7 @@ struct NormArgs {
   const uint16_t *x;
   const void *r;
   const void *w;
-  float eps;
+  float eps, inv_k;   // inv_k: 1 / K
   int64_t M, K;
   void *h;
   uint16_t *y;
@@ -25,9 +25,7 @@ struct NormArgs {
   float *scale;
 };
 
-__device__ __forceinline__ float inv_rms(float sum, int64_t K, float eps) {
-  return __frcp_rn(__fsqrt_rn(__fadd_rn(__fdiv_rn(sum, static_cast<float>(K)), eps)));
-}
+__device__ __forceinline__ float inv_rms(float sum, float inv_k, float eps) { return rsqrtf(fmaf(sum, inv_k, eps)); }
 
 // A row per warp (WARP) or per block; vector i * T + t belongs to thread t.
 template <int NV, bool WARP, bool ALIGNED, bool HF32, bool WF32>
@@ -41,7 +39,7 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2
   const int K = static_cast<int>(a.K);
   const int64_t base = m * K;
   const int e0 = t * 8 - (ALIGNED ? 0 : static_cast<int>(base & 7));
-  float f[NV][8];
+  f2 f[NV][4];
   {
     Vec8<false> x[NV];
     Vec8<HF32> r[NV];
@@ -53,13 +51,16 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       if (a.x && a.r) {
-        float xv[8];
+        f2 xv[4];
         x[i].get(xv);
         r[i].get(f[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float h = __fadd_rn(f[i][j], xv[j]);
-          f[i][j] = HF32 ? h : bf16_round(h);
+        for (int j = 0; j < 4; ++j) f[i][j] = add2(f[i][j], xv[j]);
+        if constexpr (!HF32) {   // as it is stored
+          Vec8<false> h;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) h.w[j] = pack_bf16x2(lo2(f[i][j]), hi2(f[i][j]));
+          h.get(f[i]);
         }
       } else if (a.x) {
         x[i].get(f[i]);
@@ -68,33 +69,34 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2
       }
     }
   }
-  float sum = 0.f;
+  f2 sum2 = both(0.f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     if (a.h) store_vec<ALIGNED, HF32>(f[i], row_at<HF32>(a.h, base), e0 + i * T * 8, K);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) sum = fmaf(f[i][j], f[i][j], sum);
+    for (int j = 0; j < 4; ++j) sum2 = fma2(f[i][j], f[i][j], sum2);
   }
-  const float rstd = inv_rms(row_sum<WARP>(sum, slot_sum), K, a.eps);
+  const float rstd = inv_rms(row_sum<WARP>(lo2(sum2) + hi2(sum2), slot_sum), a.inv_k, a.eps);
   float mx = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = e0 + i * T * 8;
-    float w[8];
+    f2 w[4];
     load_cols<ALIGNED, WF32>(w, a.w, e, K);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) f[i][j] = __fmul_rn(__fmul_rn(f[i][j], rstd), w[j]);
-    if (!ALIGNED) {   // 0 * rstd is NaN where rstd is not finite: elements outside the row stay out of its maximum
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (e + j < 0 || e + j >= K) f[i][j] = 0.f;
-    } else if (e >= K) {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) f[i][j] = 0.f;
-    }
+    for (int j = 0; j < 4; ++j) f[i][j] = mul2(mul2(f[i][j], both(rstd)), w[j]);
     if (a.y) store_vec<ALIGNED, false>(f[i], a.y + base, e, K);
+    if (a.codes) {
+      if (ALIGNED ? e >= K : (e < 0 || e + 8 > K)) {   // 0 * rstd may be NaN: elements outside the row stay out of its maximum
 #pragma unroll
-    for (int j = 0; j < 8; ++j) mx = max_mag(mx, f[i][j]);
+        for (int j = 0; j < 4; ++j) {
+          auto in = [&](int k) { return k >= 0 && k < K; };
+          f[i][j] = pair2(in(e + 2 * j) ? lo2(f[i][j]) : 0.f, in(e + 2 * j + 1) ? hi2(f[i][j]) : 0.f);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) mx = max_mag(max_mag(mx, lo2(f[i][j])), hi2(f[i][j]));
+    }
   }
   if (!a.codes) return;
   const RowScale rs = row_scale(row_max<WARP>(__float_as_uint(mx), slot_max));
@@ -107,7 +109,7 @@ struct NormGradArgs {
   const uint16_t *dy;
   const void *h;
   const void *w;
-  float eps;
+  float eps, inv_k;
   const void *dr;
   int64_t M, K;
   void *dh;
@@ -121,108 +123,155 @@ struct Sums {
   float hh, wdyh;
 };
 template <bool WARP>
-__device__ __forceinline__ Sums row_sums(float hh, float wdyh, float2 *slot) {
-  hh = warp_sum(hh);
-  wdyh = warp_sum(wdyh);
-  if constexpr (WARP) return {hh, wdyh};
+__device__ __forceinline__ Sums row_sums(f2 hh, f2 wdyh, float2 *slot) {
+  float v = warp_sum2(lo2(hh) + hi2(hh), lo2(wdyh) + hi2(wdyh));
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if (lane == 0) slot[threadIdx.x >> 5] = make_float2(hh, wdyh);
-  __syncthreads();
-  const float2 v = lane < warps ? slot[lane] : make_float2(0.f, 0.f);
-  return {warp_sum(v.x), warp_sum(v.y)};
+  if constexpr (!WARP) {
+    float *s = reinterpret_cast<float *>(slot);   // 32 sums hh, then 32 sums w dy h
+    if ((lane & 15) == 0) s[(threadIdx.x >> 5) + 2 * (lane & 16)] = v;
+    __syncthreads();
+    v = warp_sum2(lane < warps ? s[lane] : 0.f, lane < warps ? s[32 + lane] : 0.f);
+  }
+  return {__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16)};
+}
+// One row's share of the sums; and what both kernels make of them: rstd, and
+// rstd^2 mean(w dy h).
+__device__ __forceinline__ void add_sums(const f2 (&h)[4], const f2 (&g)[4], const f2 (&w)[4], f2 &hh, f2 &gh) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    hh = fma2(h[j], h[j], hh);
+    gh = fma2(mul2(w[j], g[j]), h[j], gh);
+  }
 }
 
 // dh of a vector and its stores; c = rstd^2 mean(w dy h).
 template <bool ALIGNED, bool HF32>
-__device__ __forceinline__ void store_dh(const NormGradArgs &a, int64_t base, int e, int K, const float (&h)[8],
-                                         const float (&g)[8], const float (&w)[8], const float (&r)[8], float rstd,
-                                         float c) {
-  float d[8];
+__device__ __forceinline__ void store_dh(const NormGradArgs &a, int64_t base, int e, int K, const f2 (&h)[4],
+                                         const f2 (&g)[4], const f2 (&w)[4], const f2 (&r)[4], float rstd, float c) {
+  f2 d[4];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, w[j] * g[j] - h[j] * c, r[j]);
+  for (int j = 0; j < 4; ++j) d[j] = fma2(both(rstd), fma2(h[j], both(-c), mul2(w[j], g[j])), r[j]);
   if (a.dh) store_vec<ALIGNED, HF32>(d, row_at<HF32>(a.dh, base), e, K);
   if (a.dx) store_vec<ALIGNED, false>(d, a.dx + base, e, K);
 }
 
-// Rows of up to 8192 elements: persistent blocks. A
-// thread keeps its columns' weight and dw sums in registers, and the next row's
-// loads are issued before the current row's sums, so that a block always has a
-// row in flight (4096 x 4096 bf16: PREFETCH). Two slots for the sums: a block
-// barrier lies between a slot's reads and its next write.
-template <int NV, bool HF32, bool WF32>
-__global__ void __launch_bounds__(512, NV == 1 && !HF32 ? 2 : 1) rmsnorm_bwd_kernel(const NormGradArgs a) {
+// 16 bytes from global to shared memory, asynchronously; a thread waits for its
+// own copies by groups. Through L1 (kHalves) where 32-byte sectors come as two
+// halves: fp32 vectors, 4096 x 4096 in fp32 65 us past L1, 46 us through it.
+template <bool kHalves>
+__device__ __forceinline__ void copy16(uint32_t smem, const void *g) {
+  if constexpr (kHalves) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Persistent blocks, a row at a time: a thread keeps its columns' weight and dw
+// sums in registers and copies its own elements of the next kDepth - 1 rows to
+// shared memory ahead of time (nobody else reads them, so there is no barrier
+// but the two of the row's sums). What bounds it is the bytes in flight: one
+// row ahead in registers instead took 28.8 us for 4096 x 4096 bf16, RING.
+// Two slots for the sums: a block barrier lies between a slot's reads and its
+// next write.
+// Shared memory of a thread's vector of one row: h, dr and dy.
+constexpr int vec_bytes(bool hf32) { return hf32 ? 80 : 48; }
+
+template <int kDepth, int NV, bool HF32, bool WF32>
+__global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a) {
   __shared__ float2 slot[2][32];
+  extern __shared__ __align__(16) uint8_t ring[];   // [depth][NV][16-byte part][thread]
+  constexpr int kH = HF32 ? 2 : 1, kParts = 2 * kH + 1;   // parts: h, dr, dy
   const int T = blockDim.x, t = threadIdx.x;
   const int K = static_cast<int>(a.K);
-  float w[NV][8], dw[NV][8];
-  Vec8<HF32> h[NV], r[NV];
-  Vec8<false> g[NV];
-  auto fetch = [&](int64_t m) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int k = (i * T + t) * 8;
-      if (m < a.M) {
-        h[i].template load<true>(row_at<HF32>(a.h, m * K), k, K);
-        g[i].template load<true>(a.dy + m * K, k, K);
-        if (a.dr) r[i].template load<true>(row_at<HF32>(a.dr, m * K), k, K);
-      }
-    }
-  };
+  f2 w[NV][4], dw[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int k = (i * T + t) * 8;
-    h[i].zero();
-    g[i].zero();
-    r[i].zero();
+    load_cols<true, WF32>(w[i], a.w, (i * T + t) * 8, K);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) dw[i][j] = 0.f;
-    load_cols<true, WF32>(w[i], a.w, k, K);
+    for (int j = 0; j < 4; ++j) dw[i][j] = both(0.f);
   }
-  int64_t m = blockIdx.x;
-  fetch(m);
-  int flip = 0;
-  for (; m < a.M; m += gridDim.x, flip ^= 1) {
-    Vec8<HF32> hc[NV], rc[NV];
-    Vec8<false> gc[NV];
+  auto part = [&](int d, int i, int q) -> uint8_t * { return ring + (((d * NV + i) * kParts + q) * T + t) * 16; };
+  auto fetch = [&](int64_t m, int d) {
+    if (m < a.M) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      hc[i] = h[i];
-      gc[i] = g[i];
-      rc[i] = r[i];
+      for (int i = 0; i < NV; ++i) {
+        const int k = (i * T + t) * 8;
+        if (k < K) {
+          const uint8_t *h = static_cast<const uint8_t *>(row_at<HF32>(a.h, m * K + k));
+          const uint8_t *r = static_cast<const uint8_t *>(row_at<HF32>(a.dr, m * K + k));
+#pragma unroll
+          for (int q = 0; q < kH; ++q) {
+            copy16<HF32>(smem_u32(part(d, i, q)), h + 16 * q);
+            if (a.dr) copy16<HF32>(smem_u32(part(d, i, kH + q)), r + 16 * q);
+          }
+          copy16<false>(smem_u32(part(d, i, 2 * kH)), a.dy + m * K + k);
+        }
+      }
     }
-    fetch(m + gridDim.x);
-    float hh = 0.f, gh = 0.f;
+    copy_commit();   // a group a row, empty past the last
+  };
+  auto read = [&](int d, int i, int q, auto &v) {
+    constexpr int n = sizeof(v.w) / 16;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4 *>(part(d, i, q + j));
+      v.w[4 * j] = u.x; v.w[4 * j + 1] = u.y; v.w[4 * j + 2] = u.z; v.w[4 * j + 3] = u.w;
+    }
+  };
+  int64_t m = blockIdx.x;
+#pragma unroll
+  for (int d = 0; d < kDepth - 1; ++d) fetch(m + static_cast<int64_t>(d) * gridDim.x, d);
+  int flip = 0, d = 0;
+  for (; m < a.M; m += gridDim.x, flip ^= 1, d = d + 1 == kDepth ? 0 : d + 1) {
+    fetch(m + static_cast<int64_t>(kDepth - 1) * gridDim.x, d == 0 ? kDepth - 1 : d - 1);
+    copy_wait<kDepth - 1>();
+    f2 hh = both(0.f), gh = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float hv[8], gv[8];
-      hc[i].get(hv);
-      gc[i].get(gv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        hh = fmaf(hv[j], hv[j], hh);
-        gh = fmaf(w[i][j] * gv[j], hv[j], gh);
+      if ((i * T + t) * 8 < K) {
+        Vec8<HF32> h;
+        Vec8<false> g;
+        f2 hv[4], gv[4];
+        read(d, i, 0, h);
+        read(d, i, 2 * kH, g);
+        h.get(hv);
+        g.get(gv);
+        add_sums(hv, gv, w[i], hh, gh);
       }
     }
     const Sums s = row_sums<false>(hh, gh, slot[flip]);
-    const float rstd = inv_rms(s.hh, K, a.eps);
-    const float c = s.wdyh / static_cast<float>(K) * rstd * rstd;
+    const float rstd = inv_rms(s.hh, a.inv_k, a.eps);
+    const float c = s.wdyh * a.inv_k * rstd * rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int k = (i * T + t) * 8;
-      float hv[8], gv[8], rv[8];
-      hc[i].get(hv);
-      gc[i].get(gv);
-      rc[i].get(rv);
+      if (k < K) {
+        Vec8<HF32> h, r;
+        Vec8<false> g;
+        f2 hv[4], gv[4], rv[4] = {};
+        read(d, i, 0, h);
+        read(d, i, 2 * kH, g);
+        h.get(hv);
+        g.get(gv);
+        if (a.dr) {
+          read(d, i, kH, r);
+          r.get(rv);
+        }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) dw[i][j] = fmaf(gv[j], hv[j] * rstd, dw[i][j]);
-      store_dh<true, HF32>(a, m * K, k, K, hv, gv, w[i], rv, rstd, c);
+        for (int j = 0; j < 4; ++j) dw[i][j] = fma2(gv[j], mul2(hv[j], both(rstd)), dw[i][j]);
+        store_dh<true, HF32>(a, m * K, k, K, hv, gv, w[i], rv, rstd, c);
+      }
     }
   }
+  copy_wait<0>();
   if (!a.part) return;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int k = (i * T + t) * 8;
-    store_vec<true, true>(dw[i], a.part + static_cast<int64_t>(blockIdx.x) * K, k, K);
+    if (k < K) store_vec<true, true>(dw[i], a.part + static_cast<int64_t>(blockIdx.x) * K, k, K);
   }
 }
 
@@ -245,27 +294,23 @@ __global__ void __launch_bounds__(row_threads(NV, WARP)) rmsnorm_bwd_rows_kernel
     h[i].template load<ALIGNED>(row_at<HF32>(a.h, base), e0 + i * T * 8, K);
     g[i].template load<ALIGNED>(a.dy + base, e0 + i * T * 8, K);
   }
-  float hh = 0.f, gh = 0.f;
+  f2 hh = both(0.f), gh = both(0.f);
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    float hv[8], gv[8], w[8];
+    f2 hv[4], gv[4], w[4];
     load_cols<ALIGNED, WF32>(w, a.w, e0 + i * T * 8, K);
     h[i].get(hv);
     g[i].get(gv);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      hh = fmaf(hv[j], hv[j], hh);
-      gh = fmaf(w[j] * gv[j], hv[j], gh);
-    }
+    add_sums(hv, gv, w, hh, gh);
   }
   const Sums s = row_sums<WARP>(hh, gh, slot);
-  const float rstd = inv_rms(s.hh, K, a.eps);
-  const float c = s.wdyh / static_cast<float>(K) * rstd * rstd;
+  const float rstd = inv_rms(s.hh, a.inv_k, a.eps);
+  const float c = s.wdyh * a.inv_k * rstd * rstd;
   if (a.rstd && t == 0) a.rstd[m] = rstd;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = e0 + i * T * 8;
-    float hv[8], gv[8], w[8], r[8] = {};
+    f2 hv[4], gv[4], w[4], r[4] = {};
     load_cols<ALIGNED, WF32>(w, a.w, e, K);
     if (a.dr) {
       Vec8<HF32> v;
@@ -285,7 +330,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_long_kernel(const NormGradAr
   const int K = static_cast<int>(a.K);
   const int64_t base = static_cast<int64_t>(blockIdx.x) * K;
   const int e0 = static_cast<int>(threadIdx.x) * 8 - (ALIGNED ? 0 : static_cast<int>(base & 7));
-  float h[8], g[8], w[8], hh = 0.f, gh = 0.f;
+  f2 h[4], g[4], w[4], hh = both(0.f), gh = both(0.f);
   auto load = [&](int e) {
     Vec8<HF32> hv;
     Vec8<false> gv;
@@ -297,18 +342,14 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_long_kernel(const NormGradAr
   };
   for (int e = e0; e < K; e += 8192) {
     load(e);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      hh = fmaf(h[j], h[j], hh);
-      gh = fmaf(w[j] * g[j], h[j], gh);
-    }
+    add_sums(h, g, w, hh, gh);
   }
   const Sums s = row_sums<false>(hh, gh, slot);
-  const float rstd = inv_rms(s.hh, K, a.eps);
-  const float c = s.wdyh / static_cast<float>(K) * rstd * rstd;
+  const float rstd = inv_rms(s.hh, a.inv_k, a.eps);
+  const float c = s.wdyh * a.inv_k * rstd * rstd;
   if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
   for (int e = e0; e < K; e += 8192) {
-    float r[8] = {};
+    f2 r[4] = {};
     load(e);
     if (a.dr) {
       Vec8<HF32> v;
@@ -329,27 +370,25 @@ __global__ void __launch_bounds__(256)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int k = (static_cast<int>(blockIdx.x) * 32 + lane) * VEC;
   const int64_t m0 = M * blockIdx.y / gridDim.y, m1 = M * (blockIdx.y + 1) / gridDim.y;
-  float dw[VEC];
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) dw[j] = 0.f;
+  f2 dw[4] = {};
   if (k < K) {
 #pragma unroll 4
     for (int64_t m = m0 + warp; m < m1; m += 8) {
-      float g[VEC], hv[VEC];
+      const float rs = rstd[m];
       if constexpr (VEC == 8) {
+        f2 g[4], hv[4];
         load_cols<true, false>(g, dy + m * K, k, static_cast<int>(K));
         load_cols<true, HF32>(hv, row_at<HF32>(h, m * K), k, static_cast<int>(K));
-      } else {
-        g[0] = bf16_to_f32(dy[m * K + k]);
-        hv[0] = HF32 ? static_cast<const float *>(h)[m * K + k] : bf16_to_f32(static_cast<const uint16_t *>(h)[m * K + k]);
-      }
-      const float rs = rstd[m];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) dw[j] = fmaf(g[j], hv[j] * rs, dw[j]);
+        for (int j = 0; j < 4; ++j) dw[j] = fma2(g[j], mul2(hv[j], both(rs)), dw[j]);
+      } else {
+        const float hv = HF32 ? static_cast<const float *>(h)[m * K + k] : bf16_to_f32(static_cast<const uint16_t *>(h)[m * K + k]);
+        dw[0] = pair2(fmaf(bf16_to_f32(dy[m * K + k]), hv * rs, lo2(dw[0])), 0.f);
+      }
     }
   }
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) s[warp][lane * VEC + j] = dw[j];
+  for (int j = 0; j < VEC; ++j) s[warp][lane * VEC + j] = j & 1 ? hi2(dw[j >> 1]) : lo2(dw[j >> 1]);
   __syncthreads();
   const int k0 = static_cast<int>(blockIdx.x) * 32 * VEC;
   for (int c = threadIdx.x; c < 32 * VEC && k0 + c < K; c += 256) {
@@ -369,6 +408,7 @@ __global__ void __launch_bounds__(1024)
   const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + c;
   float v = 0.f;
   if (k < K)
+#pragma unroll 5
     for (int i = g; i < rows; i += 32) v += part[static_cast<int64_t>(i) * K + k];
   s[g][c] = v;
   __syncthreads();
@@ -384,24 +424,38 @@ cudaError_t with_types(bool hf, bool wf, F go) {
   return wf ? go(Num<0>{}, Num<1>{}) : go(Num<0>{}, Num<0>{});
 }
 
-// The backward's shape: persistent blocks (their count), or a row kernel and,
-// for the weight's gradient, shares of the rows after it.
+// The backward's shape. Persistent blocks (`parts` of them), where K is a
+// multiple of 8 and `depth` rows fit in shared memory: one vector a thread up to
+// 512 threads, then two; as many blocks a SM as leave it about 1024 threads;
+// three rows deep where that leaves room for two blocks (or all of them). Or
+// a row kernel and, for the weight's gradient, `parts` shares of the rows after it.
 struct GradPlan {
   bool persistent;
-  int parts;
+  int parts, nv, threads, depth;
+  size_t smem;
 };
-GradPlan grad_plan(int64_t M, int64_t K) {
-  const int64_t sms = device_sm_count();
-  if (K % 8 == 0 && K <= 8192) {
-    const int64_t threads = (K / 8 + 31) / 32 * 32;
-    int64_t per_sm = 1024 / threads;   // blocks a SM
-    per_sm = per_sm < 2 ? 2 : (per_sm > 8 ? 8 : per_sm);
-    return {true, static_cast<int>(M < per_sm * sms ? M : per_sm * sms)};
+GradPlan grad_plan(int64_t M, int64_t K, bool hf) {
+  const int64_t sms = device_sm_count(), v = K / 8;
+  GradPlan g{};
+  g.nv = v <= 512 ? 1 : 2;
+  g.threads = static_cast<int>((v + 32 * g.nv - 1) / (32 * g.nv) * 32);
+  const size_t row = static_cast<size_t>(g.nv) * g.threads * vec_bytes(hf);
+  if (K % 8 == 0 && g.threads <= 1024 && 2 * row <= 220 * 1024) {
+    auto fit = [&](int depth) { return static_cast<int64_t>(222 * 1024 / (depth * row + 1024)); };
+    int64_t per_sm = 1024 / g.threads;
+    per_sm = per_sm > 8 ? 8 : per_sm;
+    g.depth = fit(3) >= (per_sm < 2 ? per_sm : 2) ? 3 : 2;
+    if (per_sm > fit(g.depth)) per_sm = fit(g.depth);
+    g.smem = g.depth * row;
+    g.persistent = true;
+    g.parts = static_cast<int>(M < per_sm * sms ? M : per_sm * sms);
+    return g;
   }
   const int64_t cols = K % 8 ? (K + 31) / 32 : (K + 255) / 256;
   int64_t parts = (4 * sms + cols - 1) / cols, most = (M + 31) / 32;   // 32 rows a block or more
   if (parts > most) parts = most;
-  return {false, static_cast<int>(parts < 1 ? 1 : parts)};
+  g.parts = static_cast<int>(parts < 1 ? 1 : parts);
+  return g;
 }
 size_t round16(size_t b) { return (b + 15) / 16 * 16; }
 
@@ -424,7 +478,7 @@ cudaError_t dw_from_rows(const NormGradArgs &a, bool hf, const GradPlan &gp, flo
 
 cudaError_t launch_rmsnorm_fwd(const uint16_t *X, const void *R, bool hf, const void *w, bool wf, float eps, int64_t M,
                                int64_t K, void *H, uint16_t *Y, int8_t *codes, float *scale, cudaStream_t st) {
-  const NormArgs a{X, R, w, eps, M, K, H, Y, codes, scale};
+  const NormArgs a{X, R, w, eps, 1.f / static_cast<float>(K), M, K, H, Y, codes, scale};
   const RowPlan p = row_plan(M, K, device_sm_count(), 2);
   return dispatch_row(p, [&](auto nv, auto warp, auto aligned) {
     return with_types(hf, wf, [&](auto h32, auto w32) {
@@ -435,26 +489,35 @@ cudaError_t launch_rmsnorm_fwd(const uint16_t *X, const void *R, bool hf, const 
   });
 }
 
+// The caller does not say the stream's type: the larger of the two.
 size_t rmsnorm_bwd_ws_bytes(int64_t M, int64_t K) {
-  const GradPlan g = grad_plan(M, K);
-  const size_t part = static_cast<size_t>(g.parts) * K * 4;
-  return g.persistent ? part : round16(static_cast<size_t>(M) * 4) + part;
+  size_t most = 0;
+  for (const bool hf : {false, true}) {
+    const GradPlan g = grad_plan(M, K, hf);
+    const size_t b = static_cast<size_t>(g.parts) * K * 4 + (g.persistent ? 0 : round16(static_cast<size_t>(M) * 4));
+    most = b > most ? b : most;
+  }
+  return most;
 }
 
 cudaError_t launch_rmsnorm_bwd(const uint16_t *dY, const void *H, bool hf, const void *w, bool wf, float eps,
                                const void *dR, int64_t M, int64_t K, void *dH, uint16_t *dX, float *dW, void *ws,
                                cudaStream_t st) {
-  NormGradArgs a{dY, H, w, eps, dR, M, K, dH, dX, nullptr, nullptr};
-  const GradPlan gp = grad_plan(M, K);
+  NormGradArgs a{dY, H, w, eps, 1.f / static_cast<float>(K), dR, M, K, dH, dX, nullptr, nullptr};
+  const GradPlan gp = grad_plan(M, K, hf);
   cudaError_t e;
   if (gp.persistent) {
     a.part = dW ? static_cast<float *>(ws) : nullptr;
-    const int64_t v = K / 8;
-    const int nv = v <= 512 ? 1 : 2, threads = static_cast<int>((v + 32 * nv - 1) / (32 * nv) * 32);
-    e = with_types(hf, wf, [&](auto h32, auto w32) {
-      if (nv == 1) rmsnorm_bwd_kernel<1, h32.value, w32.value><<<gp.parts, threads, 0, st>>>(a);
-      else rmsnorm_bwd_kernel<2, h32.value, w32.value><<<gp.parts, threads, 0, st>>>(a);
+    auto go = [&](auto kernel) {
+      const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(gp.smem));
+      if (e != cudaSuccess) return e;
+      kernel<<<gp.parts, gp.threads, gp.smem, st>>>(a);
       return cudaGetLastError();
+    };
+    e = with_types(hf, wf, [&](auto h32, auto w32) {
+      if (gp.depth == 3)
+        return gp.nv == 1 ? go(rmsnorm_bwd_kernel<3, 1, h32.value, w32.value>) : go(rmsnorm_bwd_kernel<3, 2, h32.value, w32.value>);
+      return gp.nv == 1 ? go(rmsnorm_bwd_kernel<2, 1, h32.value, w32.value>) : go(rmsnorm_bwd_kernel<2, 2, h32.value, w32.value>);
     });
   } else {
     if (dW) a.rstd = static_cast<float *>(ws);

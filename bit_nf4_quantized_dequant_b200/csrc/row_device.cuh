@@ -20,7 +20,35 @@
 namespace qlora {
 
 __device__ __forceinline__ float bf16_to_f32(uint16_t b) { return __uint_as_float(static_cast<uint32_t>(b) << 16); }
-__device__ __forceinline__ float bf16_round(float x) { return __uint_as_float(pack_bf16x2(x, 0.f) << 16); }
+
+// Two fp32 values in one 64-bit register: sm_100 multiplies and adds such pairs
+// in one instruction, each half rounded as the scalar operation would. These
+// kernels are as much bound by instructions as by memory (the norm's gradient
+// with scalar operations: 50 instructions an element, 77% of the issue slots).
+using f2 = unsigned long long;
+__device__ __forceinline__ f2 pair2(float lo, float hi) {
+  f2 d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(lo), "f"(hi));
+  return d;
+}
+__device__ __forceinline__ f2 both(float v) { return pair2(v, v); }
+__device__ __forceinline__ float lo2(f2 v) { return __uint_as_float(static_cast<uint32_t>(v)); }
+__device__ __forceinline__ float hi2(f2 v) { return __uint_as_float(static_cast<uint32_t>(v >> 32)); }
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 
 // Eight elements kept as they were loaded: four words of bf16, eight of fp32.
 template <bool F32>
@@ -31,16 +59,11 @@ struct Vec8 {
 #pragma unroll
     for (int j = 0; j < kWords; ++j) w[j] = 0u;
   }
-  __device__ __forceinline__ void get(float (&f)[8]) const {
-    if constexpr (F32) {
+  __device__ __forceinline__ void get(f2 (&f)[4]) const {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) f[j] = __uint_as_float(w[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        f[2 * j] = __uint_as_float(w[j] << 16);
-        f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-      }
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (F32) f[j] = pair2(__uint_as_float(w[2 * j]), __uint_as_float(w[2 * j + 1]));
+      else f[j] = pair2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u));
     }
   }
   // Elements e .. e + 7 of a row of K; those outside it are zero.
@@ -71,23 +94,30 @@ struct Vec8 {
 
 // Elements e .. e + 7 of a per-column vector (zero outside 0 .. K - 1).
 template <bool ALIGNED, bool F32>
-__device__ __forceinline__ void load_cols(float (&f)[8], const void *p, int e, int K) {
+__device__ __forceinline__ void load_cols(f2 (&f)[4], const void *p, int e, int K) {
   if constexpr (ALIGNED) {
     Vec8<F32> v;
     v.template load<true>(p, e, K);
     v.get(f);
   } else {
+    auto at = [&](int k) -> float {
+      if (k < 0 || k >= K) return 0.f;
+      if constexpr (F32) return static_cast<const float *>(p)[k];
+      else return bf16_to_f32(static_cast<const uint16_t *>(p)[k]);
+    };
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const bool in = e + j >= 0 && e + j < K;
-      if constexpr (F32) f[j] = in ? static_cast<const float *>(p)[e + j] : 0.f;
-      else f[j] = in ? bf16_to_f32(static_cast<const uint16_t *>(p)[e + j]) : 0.f;
-    }
+    for (int j = 0; j < 4; ++j) f[j] = pair2(at(e + 2 * j), at(e + 2 * j + 1));
   }
 }
 
 template <bool ALIGNED, bool F32>
-__device__ __forceinline__ void store_vec(const float (&f)[8], void *row, int e, int K) {
+__device__ __forceinline__ void store_vec(const f2 (&v)[4], void *row, int e, int K) {
+  float f[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    f[2 * j] = lo2(v[j]);
+    f[2 * j + 1] = hi2(v[j]);
+  }
   if (ALIGNED ? e < K : (e >= 0 && e + 8 <= K)) {
     if constexpr (F32) {
       float4 *p = reinterpret_cast<float4 *>(static_cast<float *>(row) + e);
@@ -127,6 +157,15 @@ __device__ __forceinline__ void *row_at(void *p, int64_t i) {
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// The sums of two values: of `a` in lanes 0 to 15, of `b` in the others, with
+// one exchange a step for both.
+__device__ __forceinline__ float warp_sum2(float a, float b) {
+  const bool high = (threadIdx.x & 16) != 0;
+  float v = (high ? b : a) + __shfl_xor_sync(0xffffffffu, high ? a : b, 16);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 template <bool WARP>
@@ -182,22 +221,30 @@ __device__ __forceinline__ RowScale row_scale(uint32_t max_bits) {
 
 // Codes of elements e .. e + 7 of a row of K.
 template <bool ALIGNED>
-__device__ __forceinline__ void store_codes(const float (&f)[8], const RowScale &r, int8_t *row, int e, int K) {
+__device__ __forceinline__ void store_codes(const f2 (&f)[4], const RowScale &r, int8_t *row, int e, int K) {
   uint32_t c[8];
-  float off = 0.f;   // the farthest of the values from its code
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const float m = __fmaf_rn(f[j], r.inv, kRoundMagic);
-    off = fmaxf(off, fabsf(__fmaf_rn(f[j], r.inv, -(m - kRoundMagic))));
-    c[j] = __float_as_uint(m);
-  }
-  if (r.zero) {
+  if (r.zero) {   // the same for the whole row, as is r.divide
 #pragma unroll
     for (int j = 0; j < 8; ++j) c[j] = 0u;
-  } else if (r.divide || off > 0.4999f) {
+  } else {
+    float off = 0.f;   // the farthest of the values from its code
+    const f2 inv = both(r.inv), magic = both(kRoundMagic), back = both(-kRoundMagic);
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      c[j] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(f[j], r.s)), -127.f), 127.f)));
+    for (int j = 0; j < 4; ++j) {
+      const f2 m = fma2(f[j], inv, magic);
+      // code - v / s; the subtraction of the magic number is exact
+      const f2 d = fma2(f[j], both(-r.inv), add2(m, back));
+      off = fmaxf(fmaxf(off, fabsf(lo2(d))), fabsf(hi2(d)));
+      c[2 * j] = static_cast<uint32_t>(m);
+      c[2 * j + 1] = static_cast<uint32_t>(m >> 32);
+    }
+    if (r.divide || off > 0.4999f) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float v = j & 1 ? hi2(f[j >> 1]) : lo2(f[j >> 1]);
+        c[j] = static_cast<uint32_t>(static_cast<int>(fminf(fmaxf(rintf(__fdiv_rn(v, r.s)), -127.f), 127.f)));
+      }
+    }
   }
   if (ALIGNED ? e < K : (e >= 0 && e + 8 <= K)) {
     uint32_t w[2];
