@@ -12,19 +12,20 @@
 namespace qlora {
 namespace {
 
-template <bool F32, bool ALIGNED>
-__device__ __forceinline__ void scaled(f2 (&f)[4], const Vec8<F32> &v, const float *col_scale, int e, int K) {
+template <bool F32, bool COLS>
+__device__ __forceinline__ void scaled(f2 (&f)[4], const Vec8<F32> &v, const f2 (&c)[4]) {
   v.get(f);
-  if (col_scale) {
-    f2 c[4];
-    load_cols<ALIGNED, true>(c, col_scale, e, K);
+  if constexpr (COLS) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[j] = mul2(f[j], c[j]);
   }
 }
 
-// A row per warp (WARP) or per block; vector i * T + t belongs to thread t.
-template <int NV, bool WARP, bool ALIGNED, bool F32>
+// A row per warp (WARP) or per block; vector i * T + t belongs to thread t. The
+// row stays in registers as it was loaded (a bf16 row in half of what its fp32
+// values take, so that three blocks fit a SM where two would) and is unpacked,
+// and scaled by its columns (COLS), twice.
+template <int NV, bool WARP, bool ALIGNED, bool F32, bool COLS>
 __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 1 || NV == 8 ? 1 : (F32 ? 2 : 3)))
     i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int K,
                        int8_t *__restrict__ codes, float *__restrict__ scale) {
@@ -34,31 +35,32 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 1 || 
   const int64_t m = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
   if (WARP && m >= M) return;
   const void *row = row_at<F32>(X, m * K);
-  const int phase = ALIGNED ? 0 : static_cast<int>((m * K) & 7);
+  const int e0 = t * 8 - (ALIGNED ? 0 : static_cast<int>((m * K) & 7));
   Vec8<F32> v[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) v[i].template load<ALIGNED>(row, (i * T + t) * 8 - phase, K);
-  float mx = 0.f;
+  for (int i = 0; i < NV; ++i) v[i].template load<ALIGNED>(row, e0 + i * T * 8, K);
+  Magnitude mag;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    f2 f[4];
-    scaled<F32, ALIGNED>(f, v[i], col_scale, (i * T + t) * 8 - phase, K);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mx = max_mag(max_mag(mx, lo2(f[j])), hi2(f[j]));
+    f2 f[4], c[4];
+    if constexpr (COLS) load_cols<ALIGNED, true>(c, col_scale, e0 + i * T * 8, K);
+    scaled<F32, COLS>(f, v[i], c);
+    mag.add(f);
+    v[i].forget();
   }
-  const RowScale rs = row_scale(row_max<WARP>(__float_as_uint(mx), slot));
+  const RowScale rs = row_scale(row_max<WARP>(mag.bits(), slot));
   if (t == 0) scale[m] = rs.s;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int e = (i * T + t) * 8 - phase;
-    f2 f[4];
-    scaled<F32, ALIGNED>(f, v[i], col_scale, e, K);
-    store_codes<ALIGNED>(f, rs, codes + m * K, e, K);
+    f2 f[4], c[4];
+    if constexpr (COLS) load_cols<ALIGNED, true>(c, col_scale, e0 + i * T * 8, K);
+    scaled<F32, COLS>(f, v[i], c);
+    store_codes<ALIGNED>(f, rs, codes + m * K, e0 + i * T * 8, K);
   }
 }
 
 // Rows too long for registers: read twice (the second time mostly from L2).
-template <bool ALIGNED, bool F32>
+template <bool ALIGNED, bool F32, bool COLS>
 __global__ void __launch_bounds__(1024)
     i8_quantize_long_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int K,
                             int8_t *__restrict__ codes, float *__restrict__ scale) {
@@ -66,52 +68,49 @@ __global__ void __launch_bounds__(1024)
   const int64_t m = blockIdx.x;
   const void *row = row_at<F32>(X, m * K);
   const int e0 = static_cast<int>(threadIdx.x) * 8 - (ALIGNED ? 0 : static_cast<int>((m * K) & 7));
-  float mx = 0.f;
+  Magnitude mag;
   for (int e = e0; e < K; e += 8192) {
     Vec8<F32> v;
-    f2 f[4];
+    f2 f[4], c[4];
     v.template load<ALIGNED>(row, e, K);
-    scaled<F32, ALIGNED>(f, v, col_scale, e, K);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) mx = max_mag(max_mag(mx, lo2(f[j])), hi2(f[j]));
+    if constexpr (COLS) load_cols<ALIGNED, true>(c, col_scale, e, K);
+    scaled<F32, COLS>(f, v, c);
+    mag.add(f);
   }
-  const RowScale rs = row_scale(row_max<false>(__float_as_uint(mx), slot));
+  const RowScale rs = row_scale(row_max<false>(mag.bits(), slot));
   if (threadIdx.x == 0) scale[m] = rs.s;
   for (int e = e0; e < K; e += 8192) {
     Vec8<F32> v;
-    f2 f[4];
+    f2 f[4], c[4];
     v.template load<ALIGNED>(row, e, K);
-    scaled<F32, ALIGNED>(f, v, col_scale, e, K);
+    if constexpr (COLS) load_cols<ALIGNED, true>(c, col_scale, e, K);
+    scaled<F32, COLS>(f, v, c);
     store_codes<ALIGNED>(f, rs, codes + m * K, e, K);
   }
 }
 
-// K a multiple of 16: a block takes 512 vectors of 16 codes of one row.
+// K a multiple of 8: a block takes 1024 vectors of 8 codes of one row.
 __global__ void __launch_bounds__(256)
     i8_dequantize_rows_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int K, int blocks_a_row,
                               uint16_t *__restrict__ out) {
   const uint32_t m = blockIdx.x / static_cast<uint32_t>(blocks_a_row), b = blockIdx.x - m * static_cast<uint32_t>(blocks_a_row);
   const float s = scale[m];
   const int64_t base = static_cast<int64_t>(m) * K;
-  const int k0 = static_cast<int>(b) * 8192 + static_cast<int>(threadIdx.x) * 16;
-  uint4 u[2];
+  const int k0 = static_cast<int>(b) * 8192 + static_cast<int>(threadIdx.x) * 8;
+  uint2 u[4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-    if (k0 + i * 4096 < K) u[i] = *reinterpret_cast<const uint4 *>(codes + base + k0 + i * 4096);
+  for (int i = 0; i < 4; ++i)
+    if (k0 + i * 2048 < K) u[i] = *reinterpret_cast<const uint2 *>(codes + base + k0 + i * 2048);
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    if (k0 + i * 4096 < K) {
-      const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+  for (int i = 0; i < 4; ++i) {
+    if (k0 + i * 2048 < K) {
+      f2 f[4];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        f2 f[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          auto code = [&](int b) { return static_cast<float>(static_cast<int8_t>(w[2 * h + (b >> 2)] >> (8 * (b & 3)))); };
-          f[j] = mul2(pair2(code(2 * j), code(2 * j + 1)), both(s));
-        }
-        store_vec<true, false>(f, out + base, k0 + i * 4096 + 8 * h, K);
+      for (int j = 0; j < 4; ++j) {
+        auto code = [&](int b) { return static_cast<float>(static_cast<int8_t>((b < 4 ? u[i].x : u[i].y) >> (8 * (b & 3)))); };
+        f[j] = mul2(pair2(code(2 * j), code(2 * j + 1)), both(s));
       }
+      store_vec<true, false>(f, out + base, k0 + i * 2048, K);
     }
   }
 }
@@ -156,22 +155,26 @@ cudaError_t launch_i8_quantize(const void *X, bool f32, int64_t M, int64_t K, co
   const RowPlan p = row_plan(M, K, device_sm_count(), 4);
   const int k = static_cast<int>(K);
   if (p.nv == 0) {
-    const unsigned grid = static_cast<unsigned>(M);
-    if (p.aligned && f32) i8_quantize_long_kernel<true, true><<<grid, 1024, 0, st>>>(X, cs, M, k, codes, scale);
-    else if (p.aligned) i8_quantize_long_kernel<true, false><<<grid, 1024, 0, st>>>(X, cs, M, k, codes, scale);
-    else if (f32) i8_quantize_long_kernel<false, true><<<grid, 1024, 0, st>>>(X, cs, M, k, codes, scale);
-    else i8_quantize_long_kernel<false, false><<<grid, 1024, 0, st>>>(X, cs, M, k, codes, scale);
+    auto run = [&](auto aligned, auto f32, auto cols) {
+      i8_quantize_long_kernel<aligned.value, f32.value, cols.value>
+          <<<static_cast<unsigned>(M), 1024, 0, st>>>(X, cs, M, k, codes, scale);
+    };
+    auto with = [&](auto aligned) {
+      if (f32) cs ? run(aligned, Num<1>{}, Num<1>{}) : run(aligned, Num<1>{}, Num<0>{});
+      else cs ? run(aligned, Num<0>{}, Num<1>{}) : run(aligned, Num<0>{}, Num<0>{});
+    };
+    p.aligned ? with(Num<1>{}) : with(Num<0>{});
     return cudaGetLastError();
   }
   return dispatch_row(p, [&](auto nv, auto warp, auto aligned) {
     if constexpr (nv.value == 2 && !warp.value) return cudaErrorInvalidValue;   // not a plan of this launch
     else {
-      if (f32)
-        i8_quantize_kernel<nv.value, warp.value, aligned.value, true>
+      auto run = [&](auto f32, auto cols) {
+        i8_quantize_kernel<nv.value, warp.value, aligned.value, f32.value, cols.value>
             <<<row_grid(p, M), p.threads, 0, st>>>(X, cs, M, k, codes, scale);
-      else
-        i8_quantize_kernel<nv.value, warp.value, aligned.value, false>
-            <<<row_grid(p, M), p.threads, 0, st>>>(X, cs, M, k, codes, scale);
+      };
+      if (f32) cs ? run(Num<1>{}, Num<1>{}) : run(Num<1>{}, Num<0>{});
+      else cs ? run(Num<0>{}, Num<1>{}) : run(Num<0>{}, Num<0>{});
       return cudaGetLastError();
     }
   });
@@ -180,7 +183,7 @@ cudaError_t launch_i8_quantize(const void *X, bool f32, int64_t M, int64_t K, co
 cudaError_t launch_i8_dequantize(const int8_t *codes, const float *scale, int64_t M, int64_t K, uint16_t *out,
                                  cudaStream_t st) {
   const int64_t a_row = (K + 8191) / 8192;
-  if (K % 16 == 0 && M * a_row < (int64_t(1) << 31))
+  if (K % 8 == 0 && M * a_row < (int64_t(1) << 31))
     i8_dequantize_rows_kernel<<<static_cast<unsigned>(M * a_row), 256, 0, st>>>(codes, scale, static_cast<int>(K),
                                                                                 static_cast<int>(a_row), out);
   else

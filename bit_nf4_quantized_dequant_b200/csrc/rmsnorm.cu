@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2
     for (int j = 0; j < 4; ++j) sum2 = fma2(f[i][j], f[i][j], sum2);
   }
   const float rstd = inv_rms(row_sum<WARP>(lo2(sum2) + hi2(sum2), slot_sum), a.inv_k, a.eps);
-  float mx = 0.f;
+  Magnitude mag;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = e0 + i * T * 8;
@@ -94,12 +94,11 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2
           f[i][j] = pair2(in(e + 2 * j) ? lo2(f[i][j]) : 0.f, in(e + 2 * j + 1) ? hi2(f[i][j]) : 0.f);
         }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) mx = max_mag(max_mag(mx, lo2(f[i][j])), hi2(f[i][j]));
+      mag.add(f[i]);
     }
   }
   if (!a.codes) return;
-  const RowScale rs = row_scale(row_max<WARP>(__float_as_uint(mx), slot_max));
+  const RowScale rs = row_scale(row_max<WARP>(mag.bits(), slot_max));
   if (t == 0) a.scale[m] = rs.s;
 #pragma unroll
   for (int i = 0; i < NV; ++i) store_codes<ALIGNED>(f[i], rs, a.codes + base, e0 + i * T * 8, K);
@@ -153,20 +152,6 @@ __device__ __forceinline__ void store_dh(const NormGradArgs &a, int64_t base, in
   for (int j = 0; j < 4; ++j) d[j] = fma2(both(rstd), fma2(h[j], both(-c), mul2(w[j], g[j])), r[j]);
   if (a.dh) store_vec<ALIGNED, HF32>(d, row_at<HF32>(a.dh, base), e, K);
   if (a.dx) store_vec<ALIGNED, false>(d, a.dx + base, e, K);
-}
-
-// 16 bytes from global to shared memory, asynchronously; a thread waits for its
-// own copies by groups. Through L1 (kHalves) where 32-byte sectors come as two
-// halves: fp32 vectors, 4096 x 4096 in fp32 65 us past L1, 46 us through it.
-template <bool kHalves>
-__device__ __forceinline__ void copy16(uint32_t smem, const void *g) {
-  if constexpr (kHalves) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
-  else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // Persistent blocks, a row at a time: a thread keeps its columns' weight and dw
@@ -372,7 +357,7 @@ __global__ void __launch_bounds__(256)
   const int64_t m0 = M * blockIdx.y / gridDim.y, m1 = M * (blockIdx.y + 1) / gridDim.y;
   f2 dw[4] = {};
   if (k < K) {
-#pragma unroll 4
+#pragma unroll 8
     for (int64_t m = m0 + warp; m < m1; m += 8) {
       const float rs = rstd[m];
       if constexpr (VEC == 8) {
@@ -452,7 +437,7 @@ GradPlan grad_plan(int64_t M, int64_t K, bool hf) {
     return g;
   }
   const int64_t cols = K % 8 ? (K + 31) / 32 : (K + 255) / 256;
-  int64_t parts = (4 * sms + cols - 1) / cols, most = (M + 31) / 32;   // 32 rows a block or more
+  int64_t parts = (8 * sms + cols - 1) / cols, most = (M + 15) / 16;   // 16 rows a block or more
   if (parts > most) parts = most;
   g.parts = static_cast<int>(parts < 1 ? 1 : parts);
   return g;
