@@ -29,6 +29,8 @@ template <int NV, bool WARP, bool ALIGNED, bool F32, bool COLS>
 __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 1 || NV == 8 ? 1 : (F32 ? 2 : 3)))
     i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int K,
                        int8_t *__restrict__ codes, float *__restrict__ scale) {
+  grid_dep_wait();
+  grid_dep_launch();
   __shared__ uint32_t slot[32];
   const int T = WARP ? 32 : blockDim.x;
   const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -64,6 +66,8 @@ template <bool ALIGNED, bool F32, bool COLS>
 __global__ void __launch_bounds__(1024)
     i8_quantize_long_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int K,
                             int8_t *__restrict__ codes, float *__restrict__ scale) {
+  grid_dep_wait();
+  grid_dep_launch();
   __shared__ uint32_t slot[32];
   const int64_t m = blockIdx.x;
   const void *row = row_at<F32>(X, m * K);
@@ -93,6 +97,8 @@ __global__ void __launch_bounds__(1024)
 __global__ void __launch_bounds__(256)
     i8_dequantize_rows_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int K, int blocks_a_row,
                               uint16_t *__restrict__ out) {
+  grid_dep_wait();
+  grid_dep_launch();
   const uint32_t m = blockIdx.x / static_cast<uint32_t>(blocks_a_row), b = blockIdx.x - m * static_cast<uint32_t>(blocks_a_row);
   const float s = scale[m];
   const int64_t base = static_cast<int64_t>(m) * K;
@@ -120,6 +126,8 @@ __global__ void __launch_bounds__(256)
 __global__ void __launch_bounds__(256)
     i8_dequantize_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int64_t M, int K,
                          uint16_t *__restrict__ out) {
+  grid_dep_wait();
+  grid_dep_launch();
   const int64_t total = M * K, i = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) * 8;
   if (i >= total) return;
   // the block's first row by one division, this vector's from there
@@ -156,26 +164,24 @@ cudaError_t launch_i8_quantize(const void *X, bool f32, int64_t M, int64_t K, co
   const int k = static_cast<int>(K);
   if (p.nv == 0) {
     auto run = [&](auto aligned, auto f32, auto cols) {
-      i8_quantize_long_kernel<aligned.value, f32.value, cols.value>
-          <<<static_cast<unsigned>(M), 1024, 0, st>>>(X, cs, M, k, codes, scale);
+      return launch_dependent(i8_quantize_long_kernel<aligned.value, f32.value, cols.value>, static_cast<unsigned>(M),
+                              1024, 0, st, 1, X, cs, M, k, codes, scale);
     };
     auto with = [&](auto aligned) {
-      if (f32) cs ? run(aligned, Num<1>{}, Num<1>{}) : run(aligned, Num<1>{}, Num<0>{});
-      else cs ? run(aligned, Num<0>{}, Num<1>{}) : run(aligned, Num<0>{}, Num<0>{});
+      if (f32) return cs ? run(aligned, Num<1>{}, Num<1>{}) : run(aligned, Num<1>{}, Num<0>{});
+      return cs ? run(aligned, Num<0>{}, Num<1>{}) : run(aligned, Num<0>{}, Num<0>{});
     };
-    p.aligned ? with(Num<1>{}) : with(Num<0>{});
-    return cudaGetLastError();
+    return p.aligned ? with(Num<1>{}) : with(Num<0>{});
   }
   return dispatch_row(p, [&](auto nv, auto warp, auto aligned) {
     if constexpr (nv.value == 2 && !warp.value) return cudaErrorInvalidValue;   // not a plan of this launch
     else {
       auto run = [&](auto f32, auto cols) {
-        i8_quantize_kernel<nv.value, warp.value, aligned.value, f32.value, cols.value>
-            <<<row_grid(p, M), p.threads, 0, st>>>(X, cs, M, k, codes, scale);
+        return launch_dependent(i8_quantize_kernel<nv.value, warp.value, aligned.value, f32.value, cols.value>,
+                                row_grid(p, M), p.threads, 0, st, 1, X, cs, M, k, codes, scale);
       };
-      if (f32) cs ? run(Num<1>{}, Num<1>{}) : run(Num<1>{}, Num<0>{});
-      else cs ? run(Num<0>{}, Num<1>{}) : run(Num<0>{}, Num<0>{});
-      return cudaGetLastError();
+      if (f32) return cs ? run(Num<1>{}, Num<1>{}) : run(Num<1>{}, Num<0>{});
+      return cs ? run(Num<0>{}, Num<1>{}) : run(Num<0>{}, Num<0>{});
     }
   });
 }
@@ -184,12 +190,10 @@ cudaError_t launch_i8_dequantize(const int8_t *codes, const float *scale, int64_
                                  cudaStream_t st) {
   const int64_t a_row = (K + 8191) / 8192;
   if (K % 8 == 0 && M * a_row < (int64_t(1) << 31))
-    i8_dequantize_rows_kernel<<<static_cast<unsigned>(M * a_row), 256, 0, st>>>(codes, scale, static_cast<int>(K),
-                                                                                static_cast<int>(a_row), out);
-  else
-    i8_dequantize_kernel<<<static_cast<unsigned>((M * K + 2047) / 2048), 256, 0, st>>>(codes, scale, M,
-                                                                                       static_cast<int>(K), out);
-  return cudaGetLastError();
+    return launch_dependent(i8_dequantize_rows_kernel, static_cast<unsigned>(M * a_row), 256, 0, st, 1, codes, scale,
+                            static_cast<int>(K), static_cast<int>(a_row), out);
+  return launch_dependent(i8_dequantize_kernel, static_cast<unsigned>((M * K + 2047) / 2048), 256, 0, st, 1, codes, scale,
+                          M, static_cast<int>(K), out);
 }
 
 }  // namespace qlora

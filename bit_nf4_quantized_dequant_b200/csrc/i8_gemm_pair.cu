@@ -26,6 +26,7 @@
 #include <climits>
 
 #include "i8_gemm.cuh"
+#include "norm_i8.h"
 
 namespace qlora {
 
@@ -138,6 +139,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   cluster_sync_all();   // the peer's barriers exist before anyone signals them
   tc_fence_after();
   const uint32_t tmem = sm.tmem_holder;
+  grid_dep_launch();   // behind the allocation: a following kernel's CTAs do not take TMEM that this one still needs
+  grid_dep_wait();
 
   if (warp == 0) {
     // ---------------- producer: this CTA's tokens and features ----------------
@@ -378,10 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+using PairKernel = void(const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap, const CUtensorMap,
+                        const PairParams);
 template <bool kDx>
-const void *pair_fn(bool lora) {
-  return lora ? reinterpret_cast<const void *>(i8_pair_kernel<kDx, true>)
-              : reinterpret_cast<const void *>(i8_pair_kernel<kDx, false>);
+PairKernel *pair_fn(bool lora) {
+  return lora ? i8_pair_kernel<kDx, true> : i8_pair_kernel<kDx, false>;
 }
 
 }  // namespace
@@ -435,26 +439,14 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
                            p.feat / 2, sw);
   }
   if (!ok) return cudaErrorInvalidValue;
-  const void *fn = a.dx ? pair_fn<true>(a.r != 0) : pair_fn<false>(a.r != 0);
+  auto *fn = a.dx ? pair_fn<true>(a.r != 0) : pair_fn<false>(a.r != 0);
   static_assert(sizeof(PairBars) <= 512, "room kept for the barriers");
   const size_t smem = 1024 + bars_offset(slot, p.stages, p.r_pad) + sizeof(PairBars);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.feat_tiles) * p.tok_tiles;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = 2;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void *args[] = {&tm_w, &tm_act, &tm_out, &tm_lora_w, &tm_lora_act, &p};
-  return cudaLaunchKernelExC(&cfg, fn, args);
+  return launch_dependent(fn, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), kThreads, smem, st, 2, tm_w,
+                          tm_act, tm_out, tm_lora_w, tm_lora_act, p);
 }
 
 // Single tiles of 128 x 128 as long as one wave of CTAs holds them; past that

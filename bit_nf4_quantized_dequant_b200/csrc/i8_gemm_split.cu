@@ -19,6 +19,7 @@
 #include <atomic>
 
 #include "i8_gemm.cuh"
+#include "norm_i8.h"
 
 namespace qlora {
 
@@ -150,6 +151,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  grid_dep_launch();   // behind the allocation: a following kernel's CTAs do not take TMEM that this one still needs
+  grid_dep_wait();
 
   if (warp == 0) {
     if (elect_one()) {
@@ -288,14 +291,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
+using SplitKernel = void(const CUtensorMap, const CUtensorMap, const SplitParams);
 template <bool kDx>
-const void *split_fn(int steps) {
+SplitKernel *split_fn(int steps) {
   switch (steps) {
-    case 0: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 0>);
-    case 1: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 1>);
-    case 2: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 2>);
-    case 3: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 3>);
-    default: return reinterpret_cast<const void *>(i8_split_kernel<kDx, 4>);
+    case 0: return i8_split_kernel<kDx, 0>;
+    case 1: return i8_split_kernel<kDx, 1>;
+    case 2: return i8_split_kernel<kDx, 2>;
+    case 3: return i8_split_kernel<kDx, 3>;
+    default: return i8_split_kernel<kDx, 4>;
   }
 }
 
@@ -368,23 +372,10 @@ cudaError_t launch_i8_split(const I8GemmArgs &a, cudaStream_t st) {
                   CU_TENSOR_MAP_SWIZZLE_128B);
   if (!ok) return cudaErrorInvalidValue;
   const int steps = (a.r + 15) / 16;
-  const void *fn = a.dx ? split_fn<true>(steps) : split_fn<false>(steps);
-  cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  auto *fn = a.dx ? split_fn<true>(steps) : split_fn<false>(steps);
+  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(static_cast<unsigned>(tiles * p.split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = st;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(p.split);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  void *args[] = {&tm_w, &tm_act, &p};
-  return cudaLaunchKernelExC(&cfg, fn, args);
+  return launch_dependent(fn, static_cast<unsigned>(tiles * p.split), kThreads, smem, st, p.split, tm_w, tm_act, p);
 }
 
 }  // namespace qlora

@@ -64,6 +64,14 @@ __device__ __forceinline__ bool elect_one() {
   return pred != 0;
 }
 
+// Programmatic dependent launch. A kernel launched with
+// cudaLaunchAttributeProgrammaticStreamSerialization may start before the work
+// ahead of it on the stream has finished; grid_dep_wait returns once that work
+// is complete and its writes are visible. grid_dep_launch lets the next such
+// kernel start once every CTA of this one has called it or left.
+__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // Record the first device-side error of a call (never clears an earlier one).
 __device__ __forceinline__ void set_status(int32_t *status, int32_t code) {
   if (status) atomicCAS(status, 0, code);

@@ -30,6 +30,8 @@ __device__ __forceinline__ float inv_rms(float sum, float inv_k, float eps) { re
 // A row per warp (WARP) or per block; vector i * T + t belongs to thread t.
 template <int NV, bool WARP, bool ALIGNED, bool HF32, bool WF32>
 __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2 : 1)) rmsnorm_fwd_kernel(const NormArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
   __shared__ float slot_sum[32];
   __shared__ uint32_t slot_max[32];
   const int T = WARP ? 32 : blockDim.x;
@@ -166,6 +168,8 @@ constexpr int vec_bytes(bool hf32) { return hf32 ? 80 : 48; }
 
 template <int kDepth, int NV, bool HF32, bool WF32>
 __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
   __shared__ float2 slot[2][32];
   extern __shared__ __align__(16) uint8_t ring[];   // [depth][NV][16-byte part][thread]
   constexpr int kH = HF32 ? 2 : 1, kParts = 2 * kH + 1;   // parts: h, dr, dy
@@ -264,6 +268,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a)
 // left to rmsnorm_dw_rows_kernel, for which the row's rstd is kept.
 template <int NV, bool WARP, bool ALIGNED, bool HF32, bool WF32>
 __global__ void __launch_bounds__(row_threads(NV, WARP)) rmsnorm_bwd_rows_kernel(const NormGradArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
   __shared__ float2 slot[32];
   const int T = WARP ? 32 : blockDim.x;
   const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
@@ -311,6 +317,8 @@ __global__ void __launch_bounds__(row_threads(NV, WARP)) rmsnorm_bwd_rows_kernel
 // Rows too long for registers: read twice, the second time mostly from L2.
 template <bool ALIGNED, bool HF32, bool WF32>
 __global__ void __launch_bounds__(1024) rmsnorm_bwd_long_kernel(const NormGradArgs a) {
+  grid_dep_wait();
+  grid_dep_launch();
   __shared__ float2 slot[32];
   const int K = static_cast<int>(a.K);
   const int64_t base = static_cast<int64_t>(blockIdx.x) * K;
@@ -346,15 +354,20 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_long_kernel(const NormGradAr
 }
 
 // dw from the rows themselves, after a row kernel: a block takes 32 vectors of
-// columns and a share of the rows (blockIdx.y of gridDim.y), its eight warps
+// columns (one of `strips`) and a share of the rows, its eight warps
 // every eighth row of them; out is dw, or this share's row of partials.
 template <int VEC, bool HF32>   // VEC: 8, or 1 where K is no multiple of 8 (a column's phase changes with the row)
 __global__ void __launch_bounds__(256)
-    rmsnorm_dw_rows_kernel(const uint16_t *dy, const void *h, const float *rstd, int64_t M, int64_t K, float *out) {
+    rmsnorm_dw_rows_kernel(const uint16_t *dy, const void *h, const float *rstd, int64_t M, int64_t K, int strips,
+                           float *out) {
+  grid_dep_wait();
+  grid_dep_launch();
   __shared__ float s[8][32 * VEC];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int k = (static_cast<int>(blockIdx.x) * 32 + lane) * VEC;
-  const int64_t m0 = M * blockIdx.y / gridDim.y, m1 = M * (blockIdx.y + 1) / gridDim.y;
+  const int strip = static_cast<int>(blockIdx.x) % strips, share = static_cast<int>(blockIdx.x) / strips;
+  const int shares = static_cast<int>(gridDim.x) / strips;
+  const int k = (strip * 32 + lane) * VEC;
+  const int64_t m0 = M * share / shares, m1 = M * (share + 1) / shares;
   f2 dw[4] = {};
   if (k < K) {
 #pragma unroll 8
@@ -375,12 +388,12 @@ __global__ void __launch_bounds__(256)
 #pragma unroll
   for (int j = 0; j < VEC; ++j) s[warp][lane * VEC + j] = j & 1 ? hi2(dw[j >> 1]) : lo2(dw[j >> 1]);
   __syncthreads();
-  const int k0 = static_cast<int>(blockIdx.x) * 32 * VEC;
+  const int k0 = strip * 32 * VEC;
   for (int c = threadIdx.x; c < 32 * VEC && k0 + c < K; c += 256) {
     float v = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) v += s[i][c];
-    out[static_cast<int64_t>(blockIdx.y) * K + k0 + c] = v;
+    out[static_cast<int64_t>(share) * K + k0 + c] = v;
   }
 }
 
@@ -388,6 +401,8 @@ __global__ void __launch_bounds__(256)
 // each adding every 32nd partial, then a fixed tree.
 __global__ void __launch_bounds__(1024)
     rmsnorm_dw_kernel(const float *__restrict__ part, int rows, int64_t K, float *__restrict__ dw) {
+  grid_dep_wait();
+  grid_dep_launch();
   __shared__ float s[32][33];
   const int c = threadIdx.x & 31, g = threadIdx.x >> 5;
   const int64_t k = static_cast<int64_t>(blockIdx.x) * 32 + c;
@@ -448,15 +463,13 @@ cudaError_t dw_from_rows(const NormGradArgs &a, bool hf, const GradPlan &gp, flo
   const int64_t M = a.M, K = a.K;
   float *part = gp.parts == 1 ? dW : reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + round16(static_cast<size_t>(M) * 4));
   const unsigned vec = K % 8 ? 1 : 8;
-  const dim3 grid(static_cast<unsigned>((K + 32 * vec - 1) / (32 * vec)), static_cast<unsigned>(gp.parts));
-  if (vec == 8 && hf) rmsnorm_dw_rows_kernel<8, true><<<grid, 256, 0, st>>>(a.dy, a.h, a.rstd, M, K, part);
-  else if (vec == 8) rmsnorm_dw_rows_kernel<8, false><<<grid, 256, 0, st>>>(a.dy, a.h, a.rstd, M, K, part);
-  else if (hf) rmsnorm_dw_rows_kernel<1, true><<<grid, 256, 0, st>>>(a.dy, a.h, a.rstd, M, K, part);
-  else rmsnorm_dw_rows_kernel<1, false><<<grid, 256, 0, st>>>(a.dy, a.h, a.rstd, M, K, part);
-  const cudaError_t e = cudaGetLastError();
+  const int strips = static_cast<int>((K + 32 * vec - 1) / (32 * vec));
+  auto kernel = vec == 8 ? (hf ? rmsnorm_dw_rows_kernel<8, true> : rmsnorm_dw_rows_kernel<8, false>)
+                         : (hf ? rmsnorm_dw_rows_kernel<1, true> : rmsnorm_dw_rows_kernel<1, false>);
+  const cudaError_t e = launch_dependent(kernel, static_cast<unsigned>(strips * gp.parts), 256, 0, st, 1, a.dy, a.h,
+                                         a.rstd, M, K, strips, part);
   if (e != cudaSuccess || gp.parts == 1) return e;
-  rmsnorm_dw_kernel<<<static_cast<unsigned>((K + 31) / 32), 1024, 0, st>>>(part, gp.parts, K, dW);
-  return cudaGetLastError();
+  return launch_dependent(rmsnorm_dw_kernel, static_cast<unsigned>((K + 31) / 32), 1024, 0, st, 1, part, gp.parts, K, dW);
 }
 
 }  // namespace
@@ -467,9 +480,8 @@ cudaError_t launch_rmsnorm_fwd(const uint16_t *X, const void *R, bool hf, const 
   const RowPlan p = row_plan(M, K, device_sm_count(), 2);
   return dispatch_row(p, [&](auto nv, auto warp, auto aligned) {
     return with_types(hf, wf, [&](auto h32, auto w32) {
-      rmsnorm_fwd_kernel<nv.value, warp.value, aligned.value, h32.value, w32.value>
-          <<<row_grid(p, M), p.threads, 0, st>>>(a);
-      return cudaGetLastError();
+      return launch_dependent(rmsnorm_fwd_kernel<nv.value, warp.value, aligned.value, h32.value, w32.value>,
+                              row_grid(p, M), p.threads, 0, st, 1, a);
     });
   });
 }
@@ -496,8 +508,7 @@ cudaError_t launch_rmsnorm_bwd(const uint16_t *dY, const void *H, bool hf, const
     auto go = [&](auto kernel) {
       const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(gp.smem));
       if (e != cudaSuccess) return e;
-      kernel<<<gp.parts, gp.threads, gp.smem, st>>>(a);
-      return cudaGetLastError();
+      return launch_dependent(kernel, static_cast<unsigned>(gp.parts), gp.threads, gp.smem, st, 1, a);
     };
     e = with_types(hf, wf, [&](auto h32, auto w32) {
       if (gp.depth == 3)
@@ -511,15 +522,15 @@ cudaError_t launch_rmsnorm_bwd(const uint16_t *dY, const void *H, bool hf, const
       return with_types(hf, wf, [&](auto h32, auto w32) {
         if (p.nv == 8) {   // a row's h and dy together do not fit in registers
           const unsigned grid = static_cast<unsigned>(M);
-          if (p.aligned) rmsnorm_bwd_long_kernel<true, h32.value, w32.value><<<grid, 1024, 0, st>>>(a);
-          else rmsnorm_bwd_long_kernel<false, h32.value, w32.value><<<grid, 1024, 0, st>>>(a);
-          return cudaGetLastError();
+          return p.aligned
+                     ? launch_dependent(rmsnorm_bwd_long_kernel<true, h32.value, w32.value>, grid, 1024, 0, st, 1, a)
+                     : launch_dependent(rmsnorm_bwd_long_kernel<false, h32.value, w32.value>, grid, 1024, 0, st, 1, a);
         }
         return dispatch_row(p, [&](auto nv, auto warp, auto aligned) {
           if constexpr (nv.value < 8)
-            rmsnorm_bwd_rows_kernel<nv.value, warp.value, aligned.value, h32.value, w32.value>
-                <<<row_grid(p, M), p.threads, 0, st>>>(a);
-          return cudaGetLastError();
+            return launch_dependent(rmsnorm_bwd_rows_kernel<nv.value, warp.value, aligned.value, h32.value, w32.value>,
+                                    row_grid(p, M), p.threads, 0, st, 1, a);
+          return cudaErrorInvalidValue;
         });
       });
     };
@@ -536,8 +547,7 @@ cudaError_t launch_rmsnorm_bwd(const uint16_t *dY, const void *H, bool hf, const
     return e;
   }
   if (e != cudaSuccess || !dW) return e;
-  rmsnorm_dw_kernel<<<static_cast<unsigned>((K + 31) / 32), 1024, 0, st>>>(a.part, gp.parts, K, dW);
-  return cudaGetLastError();
+  return launch_dependent(rmsnorm_dw_kernel, static_cast<unsigned>((K + 31) / 32), 1024, 0, st, 1, a.part, gp.parts, K, dW);
 }
 
 }  // namespace qlora
