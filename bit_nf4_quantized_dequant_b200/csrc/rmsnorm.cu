@@ -162,12 +162,14 @@ __device__ __forceinline__ void store_dh(const NormGradArgs &a, int64_t base, in
 // but the two of the row's sums). What bounds it is the bytes in flight: one
 // row ahead in registers instead took 28.8 us for 4096 x 4096 bf16, RING.
 // Two slots for the sums: a block barrier lies between a slot's reads and its
-// next write.
+// next write. Where K is no multiple of 8 the blocks' count is (or each has one
+// row), so that all rows of a block have the same phase; a row's first vector
+// may then begin in the row before (read, and dropped), its last one is cut.
 // Shared memory of a thread's vector of one row: h, dr and dy.
 constexpr int vec_bytes(bool hf32) { return hf32 ? 80 : 48; }
 
-template <int kDepth, int NV, bool HF32, bool WF32>
-__global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a) {
+template <int kDepth, int NV, bool ALIGNED, bool HF32, bool WF32>
+__global__ void __launch_bounds__(NV == 1 ? 512 : 1024, NV == 1 ? 2 : 1) rmsnorm_bwd_kernel(const NormGradArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ float2 slot[2][32];
@@ -175,10 +177,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a)
   constexpr int kH = HF32 ? 2 : 1, kParts = 2 * kH + 1;   // parts: h, dr, dy
   const int T = blockDim.x, t = threadIdx.x;
   const int K = static_cast<int>(a.K);
+  const int e0 = t * 8 - (ALIGNED ? 0 : static_cast<int>((static_cast<int64_t>(blockIdx.x) * K) & 7));
   f2 w[NV][4], dw[NV][4];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    load_cols<true, WF32>(w[i], a.w, (i * T + t) * 8, K);
+    load_cols<ALIGNED, WF32>(w[i], a.w, e0 + i * T * 8, K);
 #pragma unroll
     for (int j = 0; j < 4; ++j) dw[i][j] = both(0.f);
   }
@@ -187,16 +190,19 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a)
     if (m < a.M) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int k = (i * T + t) * 8;
-        if (k < K) {
-          const uint8_t *h = static_cast<const uint8_t *>(row_at<HF32>(a.h, m * K + k));
-          const uint8_t *r = static_cast<const uint8_t *>(row_at<HF32>(a.dr, m * K + k));
+        const int e = e0 + i * T * 8;
+        if (e < K) {
+          const uint8_t *h = static_cast<const uint8_t *>(row_at<HF32>(a.h, m * K + e));
+          const uint8_t *r = static_cast<const uint8_t *>(row_at<HF32>(a.dr, m * K + e));
+          // bytes of part q of a vector of `size`-byte elements that lie before the row's end
+          auto bytes = [&](int size, int q) { return ALIGNED ? 16 : min(max((K - e) * size - 16 * q, 0), 16); };
 #pragma unroll
           for (int q = 0; q < kH; ++q) {
-            copy16<HF32>(smem_u32(part(d, i, q)), h + 16 * q);
-            if (a.dr) copy16<HF32>(smem_u32(part(d, i, kH + q)), r + 16 * q);
+            const int n = bytes(HF32 ? 4 : 2, q);
+            copy16<HF32, !ALIGNED>(smem_u32(part(d, i, q)), h + 16 * q, n);
+            if (a.dr) copy16<HF32, !ALIGNED>(smem_u32(part(d, i, kH + q)), r + 16 * q, n);
           }
-          copy16<false>(smem_u32(part(d, i, 2 * kH)), a.dy + m * K + k);
+          copy16<false, !ALIGNED>(smem_u32(part(d, i, 2 * kH)), a.dy + m * K + e, bytes(2, 0));
         }
       }
     }
@@ -210,6 +216,22 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a)
       v.w[4 * j] = u.x; v.w[4 * j + 1] = u.y; v.w[4 * j + 2] = u.z; v.w[4 * j + 3] = u.w;
     }
   };
+  // h and dy of a vector; what its first one holds of the row before becomes zero
+  auto rows_of = [&](int d, int i, f2 (&hv)[4], f2 (&gv)[4]) {
+    Vec8<HF32> h;
+    Vec8<false> g;
+    read(d, i, 0, h);
+    read(d, i, 2 * kH, g);
+    h.get(hv);
+    g.get(gv);
+    if (!ALIGNED && i == 0 && e0 < 0) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        hv[j] = pair2(e0 + 2 * j < 0 ? 0.f : lo2(hv[j]), e0 + 2 * j + 1 < 0 ? 0.f : hi2(hv[j]));
+        gv[j] = pair2(e0 + 2 * j < 0 ? 0.f : lo2(gv[j]), e0 + 2 * j + 1 < 0 ? 0.f : hi2(gv[j]));
+      }
+    }
+  };
   int64_t m = blockIdx.x;
 #pragma unroll
   for (int d = 0; d < kDepth - 1; ++d) fetch(m + static_cast<int64_t>(d) * gridDim.x, d);
@@ -220,14 +242,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a)
     f2 hh = both(0.f), gh = both(0.f);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      if ((i * T + t) * 8 < K) {
-        Vec8<HF32> h;
-        Vec8<false> g;
+      if (e0 + i * T * 8 < K) {
         f2 hv[4], gv[4];
-        read(d, i, 0, h);
-        read(d, i, 2 * kH, g);
-        h.get(hv);
-        g.get(gv);
+        rows_of(d, i, hv, gv);
         add_sums(hv, gv, w[i], hh, gh);
       }
     }
@@ -236,22 +253,18 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a)
     const float c = s.wdyh * a.inv_k * rstd * rstd;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int k = (i * T + t) * 8;
-      if (k < K) {
-        Vec8<HF32> h, r;
-        Vec8<false> g;
+      const int e = e0 + i * T * 8;
+      if (e < K) {
+        Vec8<HF32> r;
         f2 hv[4], gv[4], rv[4] = {};
-        read(d, i, 0, h);
-        read(d, i, 2 * kH, g);
-        h.get(hv);
-        g.get(gv);
+        rows_of(d, i, hv, gv);
         if (a.dr) {
           read(d, i, kH, r);
           r.get(rv);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) dw[i][j] = fma2(gv[j], mul2(hv[j], both(rstd)), dw[i][j]);
-        store_dh<true, HF32>(a, m * K, k, K, hv, gv, w[i], rv, rstd, c);
+        store_dh<ALIGNED, HF32>(a, m * K, e, K, hv, gv, w[i], rv, rstd, c);
       }
     }
   }
@@ -259,8 +272,15 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_kernel(const NormGradArgs a)
   if (!a.part) return;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int k = (i * T + t) * 8;
-    if (k < K) store_vec<true, true>(dw[i], a.part + static_cast<int64_t>(blockIdx.x) * K, k, K);
+    const int e = e0 + i * T * 8;
+    float *row = a.part + static_cast<int64_t>(blockIdx.x) * K;
+    if constexpr (ALIGNED) {
+      store_vec<true, true>(dw[i], row, e, K);
+    } else {   // the partials' rows have phases of their own
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e + j >= 0 && e + j < K) row[e + j] = j & 1 ? hi2(dw[i][j >> 1]) : lo2(dw[i][j >> 1]);
+    }
   }
 }
 
@@ -424,8 +444,8 @@ cudaError_t with_types(bool hf, bool wf, F go) {
   return wf ? go(Num<0>{}, Num<1>{}) : go(Num<0>{}, Num<0>{});
 }
 
-// The backward's shape. Persistent blocks (`parts` of them), where K is a
-// multiple of 8 and `depth` rows fit in shared memory: one vector a thread up to
+// The backward's shape. Persistent blocks (`parts` of them), where `depth` rows
+// fit in shared memory: one vector a thread up to
 // 512 threads, then two; as many blocks a SM as leave it about 1024 threads;
 // three rows deep where that leaves room for two blocks (or all of them). Or
 // a row kernel and, for the weight's gradient, `parts` shares of the rows after it.
@@ -435,12 +455,12 @@ struct GradPlan {
   size_t smem;
 };
 GradPlan grad_plan(int64_t M, int64_t K, bool hf) {
-  const int64_t sms = device_sm_count(), v = K / 8;
+  const int64_t sms = device_sm_count(), v = K % 8 ? (K + 7) / 8 + 1 : K / 8;
   GradPlan g{};
   g.nv = v <= 512 ? 1 : 2;
   g.threads = static_cast<int>((v + 32 * g.nv - 1) / (32 * g.nv) * 32);
   const size_t row = static_cast<size_t>(g.nv) * g.threads * vec_bytes(hf);
-  if (K % 8 == 0 && g.threads <= 1024 && 2 * row <= 220 * 1024) {
+  if (g.threads <= 1024 && 2 * row <= 220 * 1024) {
     auto fit = [&](int depth) { return static_cast<int64_t>(222 * 1024 / (depth * row + 1024)); };
     int64_t per_sm = 1024 / g.threads;
     per_sm = per_sm > 8 ? 8 : per_sm;
@@ -448,7 +468,8 @@ GradPlan grad_plan(int64_t M, int64_t K, bool hf) {
     if (per_sm > fit(g.depth)) per_sm = fit(g.depth);
     g.smem = g.depth * row;
     g.persistent = true;
-    g.parts = static_cast<int>(M < per_sm * sms ? M : per_sm * sms);
+    const int64_t most = K % 8 ? per_sm * sms / 8 * 8 : per_sm * sms;
+    g.parts = static_cast<int>(M < most ? M : most);
     return g;
   }
   const int64_t cols = K % 8 ? (K + 31) / 32 : (K + 255) / 256;
@@ -511,9 +532,15 @@ cudaError_t launch_rmsnorm_bwd(const uint16_t *dY, const void *H, bool hf, const
       return launch_dependent(kernel, static_cast<unsigned>(gp.parts), gp.threads, gp.smem, st, 1, a);
     };
     e = with_types(hf, wf, [&](auto h32, auto w32) {
-      if (gp.depth == 3)
-        return gp.nv == 1 ? go(rmsnorm_bwd_kernel<3, 1, h32.value, w32.value>) : go(rmsnorm_bwd_kernel<3, 2, h32.value, w32.value>);
-      return gp.nv == 1 ? go(rmsnorm_bwd_kernel<2, 1, h32.value, w32.value>) : go(rmsnorm_bwd_kernel<2, 2, h32.value, w32.value>);
+      auto with = [&](auto aligned) {
+        constexpr bool al = aligned.value;
+        if (gp.depth == 3)
+          return gp.nv == 1 ? go(rmsnorm_bwd_kernel<3, 1, al, h32.value, w32.value>)
+                            : go(rmsnorm_bwd_kernel<3, 2, al, h32.value, w32.value>);
+        return gp.nv == 1 ? go(rmsnorm_bwd_kernel<2, 1, al, h32.value, w32.value>)
+                          : go(rmsnorm_bwd_kernel<2, 2, al, h32.value, w32.value>);
+      };
+      return K % 8 ? with(Num<0>{}) : with(Num<1>{});
     });
   } else {
     if (dW) a.rstd = static_cast<float *>(ws);

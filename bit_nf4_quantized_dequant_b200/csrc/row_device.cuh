@@ -231,9 +231,12 @@ struct Magnitude {
 // 16 bytes from global to shared memory, asynchronously; a thread waits for its
 // own copies by groups. Through L1 (kHalves) where 32-byte sectors come as two
 // halves: fp32 vectors, 4096 x 4096 in fp32 65 us past L1, 46 us through it.
-template <bool kHalves>
-__device__ __forceinline__ void copy16(uint32_t smem, const void *g) {
-  if constexpr (kHalves) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+// kCut: of the 16 bytes the first `bytes` are read, the rest become zero.
+template <bool kHalves, bool kCut>
+__device__ __forceinline__ void copy16(uint32_t smem, const void *g, int bytes) {
+  if constexpr (kHalves && kCut) asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(g), "r"(bytes) : "memory");
+  else if constexpr (kHalves) asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+  else if constexpr (kCut) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(g), "r"(bytes) : "memory");
   else asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
 }
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
