@@ -289,6 +289,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       float sx[4];   // tokens g, g + 8, g + 16, g + 24
 #pragma unroll
       for (int i = 0; i < 4; ++i) sx[i] = m0 + g + 8 * i < p.M ? __ldg(p.act_scale + m0 + g + 8 * i) : 0.f;
+      float2 sw[4][4];   // the features of this warp's chunks
+      if constexpr (!kDx) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int64_t f = f0 + (half + 2 * i) * 32 + j * 8 + q2;
+            sw[i][j] = f < p.F ? __ldg(reinterpret_cast<const float2 *>(p.w_scale + f)) : make_float2(0.f, 0.f);
+          }
+      }
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.accf[buf], (n >> 1) & 1u, abort_flag, p.status))) {
         ok = false;
         break;
@@ -305,27 +315,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             v[4 * j + e] = __float_as_uint(y);
           }
       };
-      auto load_sw = [&](float2 (&sw)[4], int64_t fc) {
-        if constexpr (!kDx) {
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const int64_t f = fc + j * 8 + q2;
-            sw[j] = f < p.F ? __ldg(reinterpret_cast<const float2 *>(p.w_scale + f)) : make_float2(0.f, 0.f);
-          }
-        }
-      };
       if constexpr (kLora) {
-#pragma unroll 2
-        for (int c = half; c < chunks; c += 2) {
-          float2 sw[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = half + 2 * i;
+          if (c >= chunks) break;
           uint32_t v[2][16];
           tmem_ld_frag32(t_acc + c * 32, v[0]);
           tmem_ld_frag32(t_acc + c * 32 + (16u << 16), v[1]);
-          load_sw(sw, f0 + c * 32);
           tmem_ld_wait();
-          scale(v[0], sw, 0);
+          scale(v[0], sw[i], 0);
           tmem_st_frag32(t_acc + c * 32, v[0]);
-          scale(v[1], sw, 1);
+          scale(v[1], sw[i], 1);
           tmem_st_frag32(t_acc + c * 32 + (16u << 16), v[1]);
         }
         tmem_st_wait();
@@ -338,14 +339,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
       }
-#pragma unroll 2
-      for (int c = half; c < chunks; c += 2) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int c = half + 2 * i;
+        if (c >= chunks) break;
         const int64_t fc = f0 + c * 32;
-        float2 sw[4];
         uint32_t v[2][16];
         tmem_ld_frag32(t_acc + c * 32, v[0]);
         tmem_ld_frag32(t_acc + c * 32 + (16u << 16), v[1]);
-        if constexpr (!kLora) load_sw(sw, fc);
         tmem_ld_wait();
         if (c + 2 >= chunks) {   // this warp's part is in registers: the next tile but one may have the accumulator
           tc_fence_before();
@@ -357,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          if constexpr (!kLora) scale(v[h], sw, h);
+          if constexpr (!kLora) scale(v[h], sw[i], h);
           auto pack = [&](int i) { return pack_bf16x2(__uint_as_float(v[h][i]), __uint_as_float(v[h][i + 1])); };
 #pragma unroll
           for (int j = 0; j < 4; j += 2)
