@@ -9,6 +9,7 @@ sees pointers: a tensor that does not fit raises ``ValueError`` before the call.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
@@ -79,6 +80,12 @@ def _device(t, name):
     if dev != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
     return dev
+
+
+@functools.lru_cache(maxsize=4096)
+def _bytes(size, dev, *shape):
+    """A workspace's size on device `dev` (the current one), which goes by its SM count and the shape alone."""
+    return size(*shape)
 
 
 def _matrix(t, name):
@@ -194,7 +201,7 @@ def rmsnorm_bwd(dY, H, weight, eps: float, dres=None, dH=None, dX=None, dW=None,
     if dW is None and want_dW:
         dW = _empty((K,), _F32, dev, stream)
     if dW is not None and ws is None:
-        ws = _empty((rmsnorm_workspace(M, K),), torch.uint8, dev, stream)
+        ws = _empty((_bytes(rmsnorm_workspace, dev, M, K),), torch.uint8, dev, stream)
     _check(_library().qlora_rmsnorm_bwd(dy, h, _TYPE[ht], w, _TYPE[weight.dtype], eps, dr, M, K,
                                         _need(dH, "dH", ht, shape, dev), _opt(dX, "dX", _BF16, shape, dev),
                                         _opt(dW, "dW", _F32, (K,), dev), *_space(ws, dev), _raw(stream, dev)),
@@ -253,7 +260,7 @@ def i8_linear_dx(W: I8Matrix, dY, sT=None, A=None, dX=None, ws=None, status=None
     if dX is None:
         dX = _empty((M, K), _BF16, dev, stream)
     if ws is None:
-        ws = _empty((i8_linear_workspace(M, N, K),), torch.uint8, dev, stream)
+        ws = _empty((_bytes(i8_linear_workspace, dev, M, N, K),), torch.uint8, dev, stream)
     _check(_library().qlora_i8_linear_dx(dy, M, wq, sw, N, K, t, a, r, _need(dX, "dX", _BF16, (M, K), dev),
                                          *_space(ws, dev), _opt(status, "status", torch.int32, (1,), dev),
                                          _raw(stream, dev)), "qlora_i8_linear_dx")

@@ -41,6 +41,7 @@ constexpr uint32_t kBoxBytes = 128 * kI8Step;              // 16 KiB: 128 tokens
 constexpr int kMaxStages = 9;
 constexpr uint32_t kOutBytes = 32 * 64;                    // 32 tokens x 32 features bf16, per epilogue warp
 constexpr int kEpiWarps = 8;
+constexpr int kMaxSmem = 227 * 1024;
 
 struct PairParams {
   const float *act_scale, *w_scale;
@@ -419,7 +420,7 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
   p.feat_tiles = static_cast<int>((a.F + p.feat - 1) / p.feat);
   const uint32_t slot = slot_bytes(a.dx, p.feat);
   // what 227 KB hold beside the staging, the adapter's tiles, the barriers and the alignment
-  p.stages = static_cast<int>((232448u - 1024u - 512u - bars_offset(slot, 0, p.r_pad)) / slot);
+  p.stages = static_cast<int>((static_cast<uint32_t>(kMaxSmem) - 1024u - 512u - bars_offset(slot, 0, p.r_pad)) / slot);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
 
   CUtensorMap tm_w, tm_act, tm_out, tm_lora_w, tm_lora_act;
@@ -443,7 +444,7 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
   auto *fn = a.dx ? pair_fn<true>(a.r != 0) : pair_fn<false>(a.r != 0);
   static_assert(sizeof(PairBars) <= 512, "room kept for the barriers");
   const size_t smem = 1024 + bars_offset(slot, p.stages, p.r_pad) + sizeof(PairBars);
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = allow_smem(fn, kMaxSmem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = static_cast<int64_t>(p.feat_tiles) * p.tok_tiles;
   return launch_dependent(fn, static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs)), kThreads, smem, st, 2, tm_w,

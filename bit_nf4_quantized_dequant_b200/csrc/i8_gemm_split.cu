@@ -313,12 +313,11 @@ static int resident_clusters(int split) {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   int n = known[dev][split].load(std::memory_order_relaxed);
   if (n == 0) {
-    const void *fn = reinterpret_cast<const void *>(i8_split_kernel<false, 0>);
-    const int smem = 200 * 1024;
+    auto *fn = i8_split_kernel<false, 0>;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(split * device_sm_count()));
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = smem;
+    cfg.dynamicSmemBytes = 200 * 1024;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = static_cast<unsigned>(split);
@@ -326,7 +325,7 @@ static int resident_clusters(int split) {
     attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+    if (allow_smem(fn) != cudaSuccess ||
         cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1) {
       cudaGetLastError();   // no answer is no reason to fail: no split
       n = 1;
@@ -373,7 +372,7 @@ cudaError_t launch_i8_split(const I8GemmArgs &a, cudaStream_t st) {
   if (!ok) return cudaErrorInvalidValue;
   const int steps = (a.r + 15) / 16;
   auto *fn = a.dx ? split_fn<true>(steps) : split_fn<false>(steps);
-  const cudaError_t e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const cudaError_t e = allow_smem(fn);
   if (e != cudaSuccess) return e;
   return launch_dependent(fn, static_cast<unsigned>(tiles * p.split), kThreads, smem, st, p.split, tm_w, tm_act, p);
 }

@@ -7,6 +7,14 @@
 
 namespace qlora {
 
+// Lets a kernel use up to 220 KB (or `most`) of dynamic shared memory. Always the
+// same number for a kernel: host threads that launch it at the same time set
+// the attribute under each other's feet.
+template <class... P>
+cudaError_t allow_smem(void (*kernel)(P...), int most = 220 * 1024) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+}
+
 // Launches a kernel that begins with grid_dep_wait, so that its launch and set-up
 // overlap the end of the work ahead of it on the stream (about 2 us of a call
 // among others). cluster: CTAs of a cluster.

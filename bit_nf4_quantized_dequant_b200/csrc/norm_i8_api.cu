@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kMaxQuantCols = 65536, kMaxNormCols = 32768, kMaxContraction = 131056;
 constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxLinear = (int64_t(1) << 31) - 1024;   // tile coordinates stay in 31 bits
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 template <class... P>
@@ -31,7 +32,7 @@ qlora_status_t check_rows(int64_t M, int64_t K, int64_t most) {
 // The shapes and adapter of both products; C is the contraction's length.
 qlora_status_t check_i8_shape(int64_t M, int64_t N, int64_t K, int32_t r) {
   if (M < 1 || N < 1 || K < 1) return QLORA_ERR_INVALID_ARG;
-  if (N % 16 || K % 16 || M > kMaxRows || N > kMaxRows || K > kMaxContraction) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (N % 16 || K % 16 || M > kMaxLinear || N > kMaxLinear || K > kMaxContraction) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (r != 0 && (r < 8 || r > 64 || r % 8)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
 }
