@@ -93,7 +93,8 @@ __global__ void __launch_bounds__(1024)
   }
 }
 
-// K a multiple of 8: a block takes 1024 vectors of 8 codes of one row.
+// A block takes 1024 vectors of 8 codes of one row.
+template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
     i8_dequantize_rows_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int K, int blocks_a_row,
                               uint16_t *__restrict__ out) {
@@ -102,27 +103,37 @@ __global__ void __launch_bounds__(256)
   const uint32_t m = blockIdx.x / static_cast<uint32_t>(blocks_a_row), b = blockIdx.x - m * static_cast<uint32_t>(blocks_a_row);
   const float s = scale[m];
   const int64_t base = static_cast<int64_t>(m) * K;
-  const int k0 = static_cast<int>(b) * 8192 + static_cast<int>(threadIdx.x) * 8;
+  const int e0 = static_cast<int>(b) * 8192 + static_cast<int>(threadIdx.x) * 8 - (ALIGNED ? 0 : static_cast<int>(base & 7));
   uint2 u[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (k0 + i * 2048 < K) u[i] = *reinterpret_cast<const uint2 *>(codes + base + k0 + i * 2048);
+  for (int i = 0; i < 4; ++i) {
+    const int e = e0 + i * 2048;
+    if (ALIGNED ? e < K : (e >= 0 && e + 8 <= K)) {
+      u[i] = *reinterpret_cast<const uint2 *>(codes + base + e);
+    } else if constexpr (!ALIGNED) {
+      u[i] = make_uint2(0u, 0u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (e + j >= 0 && e + j < K)
+          (j < 4 ? u[i].x : u[i].y) |= static_cast<uint32_t>(static_cast<uint8_t>(codes[base + e + j])) << (8 * (j & 3));
+    }
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if (k0 + i * 2048 < K) {
+    if (e0 + i * 2048 < K) {
       f2 f[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         auto code = [&](int b) { return static_cast<float>(static_cast<int8_t>((b < 4 ? u[i].x : u[i].y) >> (8 * (b & 3)))); };
         f[j] = mul2(pair2(code(2 * j), code(2 * j + 1)), both(s));
       }
-      store_vec<true, false>(f, out + base, k0 + i * 2048, K);
+      store_vec<ALIGNED, false>(f, out + base, e0 + i * 2048, K);
     }
   }
 }
 
-// Any K: vectors of 8 codes over the whole matrix as one array; a vector may
-// cross into the next rows.
+// Short rows: vectors of 8 codes over the whole matrix as one array; a vector
+// may cross into the next rows.
 __global__ void __launch_bounds__(256)
     i8_dequantize_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int64_t M, int K,
                          uint16_t *__restrict__ out) {
@@ -188,10 +199,12 @@ cudaError_t launch_i8_quantize(const void *X, bool f32, int64_t M, int64_t K, co
 
 cudaError_t launch_i8_dequantize(const int8_t *codes, const float *scale, int64_t M, int64_t K, uint16_t *out,
                                  cudaStream_t st) {
-  const int64_t a_row = (K + 8191) / 8192;
-  if (K % 8 == 0 && M * a_row < (int64_t(1) << 31))
-    return launch_dependent(i8_dequantize_rows_kernel, static_cast<unsigned>(M * a_row), 256, 0, st, 1, codes, scale,
-                            static_cast<int>(K), static_cast<int>(a_row), out);
+  const int64_t a_row = (K + (K % 8 ? 7 : 0) + 8191) / 8192;   // a row off phase may touch one vector more
+  if (K >= 1024 && M * a_row < (int64_t(1) << 31)) {
+    auto *kernel = K % 8 ? i8_dequantize_rows_kernel<false> : i8_dequantize_rows_kernel<true>;
+    return launch_dependent(kernel, static_cast<unsigned>(M * a_row), 256, 0, st, 1, codes, scale, static_cast<int>(K),
+                            static_cast<int>(a_row), out);
+  }
   return launch_dependent(i8_dequantize_kernel, static_cast<unsigned>((M * K + 2047) / 2048), 256, 0, st, 1, codes, scale,
                           M, static_cast<int>(K), out);
 }
