@@ -29,7 +29,7 @@ __device__ __forceinline__ float inv_rms(float sum, float inv_k, float eps) { re
 
 // A row per warp (WARP) or per block; vector i * T + t belongs to thread t.
 template <int NV, bool WARP, bool ALIGNED, bool HF32, bool WF32>
-__global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2 : 1)) rmsnorm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? (ALIGNED ? 2 : 3) : 1)) rmsnorm_fwd_kernel(const NormArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ float slot_sum[32];
@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2
   const int K = static_cast<int>(a.K);
   const int64_t base = m * K;
   const int e0 = t * 8 - (ALIGNED ? 0 : static_cast<int>(base & 7));
-  f2 f[NV][4];
+  f2 f[NV][4], w[NV][4];
   {
     Vec8<false> x[NV];
     Vec8<HF32> r[NV];
@@ -49,6 +49,10 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2
     for (int i = 0; i < NV; ++i) {
       if (a.x) x[i].template load<ALIGNED>(a.x + base, e0 + i * T * 8, K);
       if (a.r) r[i].template load<ALIGNED>(row_at<HF32>(a.r, base), e0 + i * T * 8, K);
+    }
+    if constexpr (NV <= 2) {   // the weights too are on their way before the row's sum
+#pragma unroll
+      for (int i = 0; i < NV; ++i) load_cols<ALIGNED, WF32>(w[i], a.w, e0 + i * T * 8, K);
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -83,10 +87,9 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? 2
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = e0 + i * T * 8;
-    f2 w[4];
-    load_cols<ALIGNED, WF32>(w, a.w, e, K);
+    if constexpr (NV > 2) load_cols<ALIGNED, WF32>(w[i], a.w, e, K);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[i][j] = mul2(mul2(f[i][j], both(rstd)), w[j]);
+    for (int j = 0; j < 4; ++j) f[i][j] = mul2(mul2(f[i][j], both(rstd)), w[i][j]);
     if (a.y) store_vec<ALIGNED, false>(f[i], a.y + base, e, K);
     if (a.codes) {
       if (ALIGNED ? e >= K : (e < 0 || e + 8 > K)) {   // 0 * rstd may be NaN: elements outside the row stay out of its maximum
