@@ -27,9 +27,14 @@ struct NormArgs {
 
 __device__ __forceinline__ float inv_rms(float sum, float inv_k, float eps) { return rsqrtf(fmaf(sum, inv_k, eps)); }
 
-// A row per warp (WARP) or per block; vector i * T + t belongs to thread t.
+// A row per warp (WARP) or per block; vector i * T + t belongs to thread t. What
+// bounds it is memory: 4096 x 4096 bf16 takes 21.5 us, 134 MB at 6.2 TB/s (95% of
+// a copy's rate). Off phase the weights come element by element and three blocks
+// a SM hide that: 1001 x 5127 bf16 11.7 us, with two 13.2; with an fp32 stream
+// and int8 output 16 us, 3.4 TB/s, held by the instructions of the codes.
 template <int NV, bool WARP, bool ALIGNED, bool HF32, bool WF32>
-__global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? (ALIGNED ? 2 : 3) : 1)) rmsnorm_fwd_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? (ALIGNED ? 2 : 3) : 1))
+    rmsnorm_fwd_kernel(const NormArgs a) {
   grid_dep_wait();
   grid_dep_launch();
   __shared__ float slot_sum[32];
@@ -50,7 +55,7 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? (
       if (a.x) x[i].template load<ALIGNED>(a.x + base, e0 + i * T * 8, K);
       if (a.r) r[i].template load<ALIGNED>(row_at<HF32>(a.r, base), e0 + i * T * 8, K);
     }
-    if constexpr (NV <= 2) {   // the weights too are on their way before the row's sum
+    if constexpr (NV <= 2 && ALIGNED) {   // the weights too are on their way before the row's sum
 #pragma unroll
       for (int i = 0; i < NV; ++i) load_cols<ALIGNED, WF32>(w[i], a.w, e0 + i * T * 8, K);
     }
@@ -87,7 +92,7 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? (
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const int e = e0 + i * T * 8;
-    if constexpr (NV > 2) load_cols<ALIGNED, WF32>(w[i], a.w, e, K);
+    if constexpr (NV > 2 || !ALIGNED) load_cols<ALIGNED, WF32>(w[i], a.w, e, K);
 #pragma unroll
     for (int j = 0; j < 4; ++j) f[i][j] = mul2(mul2(f[i][j], both(rstd)), w[i][j]);
     if (a.y) store_vec<ALIGNED, false>(f[i], a.y + base, e, K);
