@@ -124,23 +124,20 @@ struct NormGradArgs {
   void *dh;
   uint16_t *dx;
   float *part;   // persistent kernel: [gridDim.x, K] partial dw
-  float *rstd;   // row kernels: [M], or null
+  float *rstd;   // long rows: [M], or null
 };
 
 // The row's two sums, over the threads that share it.
 struct Sums {
   float hh, wdyh;
 };
-template <bool WARP>
 __device__ __forceinline__ Sums row_sums(f2 hh, f2 wdyh, float2 *slot) {
   float v = warp_sum2(lo2(hh) + hi2(hh), lo2(wdyh) + hi2(wdyh));
   const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-  if constexpr (!WARP) {
-    float *s = reinterpret_cast<float *>(slot);   // 32 sums hh, then 32 sums w dy h
-    if ((lane & 15) == 0) s[(threadIdx.x >> 5) + 2 * (lane & 16)] = v;
-    __syncthreads();
-    v = warp_sum2(lane < warps ? s[lane] : 0.f, lane < warps ? s[32 + lane] : 0.f);
-  }
+  float *s = reinterpret_cast<float *>(slot);   // 32 sums hh, then 32 sums w dy h
+  if ((lane & 15) == 0) s[(threadIdx.x >> 5) + 2 * (lane & 16)] = v;
+  __syncthreads();
+  v = warp_sum2(lane < warps ? s[lane] : 0.f, lane < warps ? s[32 + lane] : 0.f);
   return {__shfl_sync(0xffffffffu, v, 0), __shfl_sync(0xffffffffu, v, 16)};
 }
 // One row's share of the sums; and what both kernels make of them: rstd, and
@@ -257,7 +254,7 @@ __global__ void __launch_bounds__(NV == 1 ? 512 : 1024, NV == 1 ? 2 : 1) rmsnorm
         add_sums(hv, gv, w[i], hh, gh);
       }
     }
-    const Sums s = row_sums<false>(hh, gh, slot[flip]);
+    const Sums s = row_sums(hh, gh, slot[flip]);
     const float rstd = inv_rms(s.hh, a.inv_k, a.eps);
     const float c = s.wdyh * a.inv_k * rstd * rstd;
 #pragma unroll
@@ -293,57 +290,9 @@ __global__ void __launch_bounds__(NV == 1 ? 512 : 1024, NV == 1 ? 2 : 1) rmsnorm
   }
 }
 
-// A row per warp or block, as the forward; the weight's gradient, if any, is
-// left to rmsnorm_dw_rows_kernel, for which the row's rstd is kept.
-template <int NV, bool WARP, bool ALIGNED, bool HF32, bool WF32>
-__global__ void __launch_bounds__(row_threads(NV, WARP)) rmsnorm_bwd_rows_kernel(const NormGradArgs a) {
-  grid_dep_wait();
-  grid_dep_launch();
-  __shared__ float2 slot[32];
-  const int T = WARP ? 32 : blockDim.x;
-  const int t = WARP ? (threadIdx.x & 31) : threadIdx.x;
-  const int64_t m = WARP ? static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
-  if (WARP && m >= a.M) return;
-  const int K = static_cast<int>(a.K);
-  const int64_t base = m * K;
-  const int e0 = t * 8 - (ALIGNED ? 0 : static_cast<int>(base & 7));
-  Vec8<HF32> h[NV];
-  Vec8<false> g[NV];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    h[i].template load<ALIGNED>(row_at<HF32>(a.h, base), e0 + i * T * 8, K);
-    g[i].template load<ALIGNED>(a.dy + base, e0 + i * T * 8, K);
-  }
-  f2 hh = both(0.f), gh = both(0.f);
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    f2 hv[4], gv[4], w[4];
-    load_cols<ALIGNED, WF32>(w, a.w, e0 + i * T * 8, K);
-    h[i].get(hv);
-    g[i].get(gv);
-    add_sums(hv, gv, w, hh, gh);
-  }
-  const Sums s = row_sums<WARP>(hh, gh, slot);
-  const float rstd = inv_rms(s.hh, a.inv_k, a.eps);
-  const float c = s.wdyh * a.inv_k * rstd * rstd;
-  if (a.rstd && t == 0) a.rstd[m] = rstd;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = e0 + i * T * 8;
-    f2 hv[4], gv[4], w[4], r[4] = {};
-    load_cols<ALIGNED, WF32>(w, a.w, e, K);
-    if (a.dr) {
-      Vec8<HF32> v;
-      v.template load<ALIGNED>(row_at<HF32>(a.dr, base), e, K);
-      v.get(r);
-    }
-    h[i].get(hv);
-    g[i].get(gv);
-    store_dh<ALIGNED, HF32>(a, base, e, K, hv, gv, w, r, rstd, c);
-  }
-}
-
-// Rows too long for registers: read twice, the second time mostly from L2.
+// Rows too long for that: a block each, read twice, the second time mostly from
+// L2. The weight's gradient, if any, is left to rmsnorm_dw_rows_kernel, for which
+// the row's rstd is kept.
 template <bool ALIGNED, bool HF32, bool WF32>
 __global__ void __launch_bounds__(1024) rmsnorm_bwd_long_kernel(const NormGradArgs a) {
   grid_dep_wait();
@@ -366,7 +315,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_bwd_long_kernel(const NormGradAr
     load(e);
     add_sums(h, g, w, hh, gh);
   }
-  const Sums s = row_sums<false>(hh, gh, slot);
+  const Sums s = row_sums(hh, gh, slot);
   const float rstd = inv_rms(s.hh, a.inv_k, a.eps);
   const float c = s.wdyh * a.inv_k * rstd * rstd;
   if (a.rstd && threadIdx.x == 0) a.rstd[blockIdx.x] = rstd;
@@ -472,7 +421,7 @@ cudaError_t with_types(bool hf, bool wf, F go) {
 // fit in shared memory: one vector a thread up to
 // 512 threads, then two; as many blocks a SM as leave it about 1024 threads;
 // three rows deep where that leaves room for two blocks (or all of them). Or
-// a row kernel and, for the weight's gradient, `parts` shares of the rows after it.
+// a block a row and, for the weight's gradient, `parts` shares of the rows after it.
 struct GradPlan {
   bool persistent;
   int parts, nv, threads, depth;
@@ -568,21 +517,11 @@ cudaError_t launch_rmsnorm_bwd(const uint16_t *dY, const void *H, bool hf, const
     });
   } else {
     if (dW) a.rstd = static_cast<float *>(ws);
-    const RowPlan p = row_plan(M, K, device_sm_count(), 2);
     auto rows = [&](const NormGradArgs &a) {
       return with_types(hf, wf, [&](auto h32, auto w32) {
-        if (p.nv == 8) {   // a row's h and dy together do not fit in registers
-          const unsigned grid = static_cast<unsigned>(M);
-          return p.aligned
-                     ? launch_dependent(rmsnorm_bwd_long_kernel<true, h32.value, w32.value>, grid, 1024, 0, st, 1, a)
-                     : launch_dependent(rmsnorm_bwd_long_kernel<false, h32.value, w32.value>, grid, 1024, 0, st, 1, a);
-        }
-        return dispatch_row(p, [&](auto nv, auto warp, auto aligned) {
-          if constexpr (nv.value < 8)
-            return launch_dependent(rmsnorm_bwd_rows_kernel<nv.value, warp.value, aligned.value, h32.value, w32.value>,
-                                    row_grid(p, M), p.threads, 0, st, 1, a);
-          return cudaErrorInvalidValue;
-        });
+        auto *kernel = K % 8 ? rmsnorm_bwd_long_kernel<false, h32.value, w32.value>
+                             : rmsnorm_bwd_long_kernel<true, h32.value, w32.value>;
+        return launch_dependent(kernel, static_cast<unsigned>(M), 1024, 0, st, 1, a);
       });
     };
     // dw is formed from dy after rstd: where dh or dx overwrites dy, they wait for it

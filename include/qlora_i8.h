@@ -8,7 +8,9 @@
  * bits. The conventions of qlora.h hold: row-major contiguous matrices, bf16 as
  * 16-bit patterns, device pointers 16-byte aligned (per-row and per-channel
  * fp32 vectors included) and in the current device's memory, nothing allocated
- * or synchronised, argument errors returned before anything is launched.
+ * or synchronised, argument errors returned before anything is launched. A call's
+ * kernels may set themselves up while earlier work on the stream still runs; they
+ * read and write nothing before it has finished.
  *
  * An int8 matrix is codes int8 [rows, cols] and scale fp32 [rows], value
  * codes * scale: one scale a token for activations, one an output channel for
