@@ -201,7 +201,8 @@ def rmsnorm_bwd(dY, H, weight, eps: float, dres=None, dH=None, dX=None, dW=None,
     if dW is None and want_dW:
         dW = _empty((K,), _F32, dev, stream)
     if dW is not None and ws is None:
-        ws = _empty((_bytes(rmsnorm_workspace, dev, M, K),), torch.uint8, dev, stream)
+        need = _bytes(rmsnorm_workspace, dev, M, K)
+        ws = _empty((need,), torch.uint8, dev, stream) if need else None
     _check(_library().qlora_rmsnorm_bwd(dy, h, _TYPE[ht], w, _TYPE[weight.dtype], eps, dr, M, K,
                                         _need(dH, "dH", ht, shape, dev), _opt(dX, "dX", _BF16, shape, dev),
                                         _opt(dW, "dW", _F32, (K,), dev), *_space(ws, dev), _raw(stream, dev)),

@@ -89,8 +89,9 @@ qlora_status_t qlora_rmsnorm_bwd(const uint16_t *dY, const void *H, int32_t h_ty
   const qlora_status_t st = check_rows(M, K, kMaxNormCols);
   if (st != QLORA_OK) return st;
   if (!all_aligned16(dY, H, weight, dR, dH, dX, dW)) return QLORA_ERR_MISALIGNED;
-  if (dW && (!ws || ws_bytes < rmsnorm_bwd_ws_bytes(M, K))) return QLORA_ERR_WORKSPACE;
-  if (dW && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
+  const size_t need = dW ? rmsnorm_bwd_ws_bytes(M, K) : 0;
+  if (need && (!ws || ws_bytes < need)) return QLORA_ERR_WORKSPACE;
+  if (need && !aligned16(ws)) return QLORA_ERR_MISALIGNED;
   return cuda_status(launch_rmsnorm_bwd(dY, H, h_type == QLORA_TYPE_F32, weight, w_type == QLORA_TYPE_F32, eps, dR, M,
                                         K, dH, dX, dW, ws, cu(stream)));
 }

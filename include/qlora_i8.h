@@ -61,7 +61,8 @@ qlora_status_t qlora_rmsnorm_fwd(const uint16_t *X, const void *R, int32_t h_typ
                                  int8_t *codes, float *scale, qlora_stream_t stream);
 
 /* Workspace bytes of qlora_rmsnorm_bwd when dW is asked for, on the current
- * device (it scales with the SM count); it needs no initialisation. The
+ * device (it scales with the SM count); 0 for a few short rows, which need
+ * none (ws may then be NULL). It needs no initialisation. The
  * workspace may be reused by consecutive calls on one stream; calls that run
  * concurrently need separate ones. Errors: INVALID_ARG, UNSUPPORTED_SHAPE. */
 qlora_status_t qlora_rmsnorm_workspace(int64_t M, int64_t K, size_t *bytes);

@@ -63,8 +63,9 @@ def test_norm_refusals(so):
     assert so.qlora_rmsnorm_workspace(4, 64, None) == INVALID
     assert so.qlora_rmsnorm_workspace(0, 64, ctypes.byref(n)) == INVALID
     assert so.qlora_rmsnorm_workspace(4, 32769, ctypes.byref(n)) == SHAPE
-    assert so.qlora_rmsnorm_workspace(4, 64, ctypes.byref(n)) == 0 and n.value > 0
-    b = lambda dy=X, h=V, ht=0, w=W, wt=0, eps=1e-5, dr=None, m=4, k=64, dh=T, dx=None, dw=Y, ws=S, nb=n.value: \
+    assert so.qlora_rmsnorm_workspace(4, 64, ctypes.byref(n)) == 0 and n.value == 0
+    assert so.qlora_rmsnorm_workspace(40, 64, ctypes.byref(n)) == 0 and n.value > 0
+    b = lambda dy=X, h=V, ht=0, w=W, wt=0, eps=1e-5, dr=None, m=40, k=64, dh=T, dx=None, dw=Y, ws=S, nb=n.value: \
         so.qlora_rmsnorm_bwd(dy, h, ht, w, wt, eps, dr, m, k, dh, dx, dw, ws, nb, None)
     assert b(dy=None) == b(h=None) == b(w=None) == b(dh=None) == b(ht=2) == b(wt=2) == b(eps=nan) == INVALID
     assert b(m=0) == b(k=0) == INVALID and b(k=32769) == SHAPE

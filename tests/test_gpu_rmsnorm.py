@@ -25,7 +25,7 @@ SUM, Y32 = 48 * U32, 32 * U32
 SHAPES = [(1, 1), (3, 7), (5, 16), (2, 31), (129, 64), (7, 129), (301, 256), (300, 264), (5, 512), (3, 1000), (2, 1024),
           (1, 4096), (301, 4096), (9, 4104), (4, 5127), (700, 2056), (2, 8191), (3, 8192), (2, 8200), (2, 11008),
           (2, 16384), (1, 16392), (2, 32761), (2, 32768), (700, 1001), (2500, 63), (320, 5127), (310, 11001),
-          (1300, 517), (600, 2), (300, 16390)]
+          (1300, 517), (600, 2), (300, 16390), (16, 4096), (16, 4095), (17, 1000), (11, 5953), (16, 130), (13, 127)]
 
 
 def _dt(torch, f32):
