@@ -99,10 +99,10 @@ def _raw(stream, dev):
     return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
-def _empty(shape, dtype, dev, stream):
-    """Memory from the current stream's pool; where another stream uses it, that is recorded."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(dev):
+def _empty(like, shape, dtype, stream):
+    """Memory on the device of `like`, from the current stream's pool; where another stream uses it, that is recorded."""
+    t = like.new_empty(shape, dtype=dtype)
+    if stream is not None and stream.cuda_stream != torch._C._cuda_getCurrentRawStream(t.get_device()):
         stream.wait_stream(torch.cuda.current_stream())   # the memory may still be in use here
         t.record_stream(stream)
     return t
@@ -134,7 +134,7 @@ def i8_quantize(X, col_scale=None, out: I8Matrix | None = None, stream=None) -> 
     dev = _device(X, "X")
     x = _need(X, "X", (_BF16, _F32), shape, dev)
     if out is None:
-        out = I8Matrix(_empty(shape, _I8, dev, stream), _empty((M,), _F32, dev, stream))
+        out = I8Matrix(_empty(X, shape, _I8, stream), _empty(X, (M,), _F32, stream))
     codes, scale = _need_i8(out, "out", shape, dev)
     _check(_library().qlora_i8_quantize(x, _TYPE[X.dtype], M, K, _opt(col_scale, "col_scale", _F32, (K,), dev),
                                         codes, scale, _raw(stream, dev)), "qlora_i8_quantize")
@@ -147,7 +147,7 @@ def i8_dequantize(q: I8Matrix, out=None, stream=None):
     dev = _device(q.codes, "codes")
     codes, scale = _need_i8(q, "q", shape, dev)
     if out is None:
-        out = _empty(shape, _BF16, dev, stream)
+        out = _empty(q.codes, shape, _BF16, stream)
     _check(_library().qlora_i8_dequantize(codes, scale, M, K, _need(out, "out", _BF16, shape, dev), _raw(stream, dev)),
            "qlora_i8_dequantize")
     return out
@@ -169,9 +169,9 @@ def rmsnorm_fwd(X, weight, eps: float, residual=None, H=None, Y=None, q: I8Matri
     r = _opt(residual, "residual", (_BF16, _F32), shape, dev)
     w = _need(weight, "weight", (_BF16, _F32), (K,), dev)
     if Y is None and q is None:
-        Y = _empty(shape, _BF16, dev, stream)
+        Y = _empty(first, shape, _BF16, stream)
     if H is None and want_H and X is not None and residual is not None:
-        H = _empty(shape, ht, dev, stream)
+        H = _empty(first, shape, ht, stream)
     codes, scale = (None, None) if q is None else _need_i8(q, "q", shape, dev)
     _check(_library().qlora_rmsnorm_fwd(x, r, _TYPE[ht], w, _TYPE[weight.dtype], eps, M, K,
                                         _opt(H, "H", ht, shape, dev), _opt(Y, "Y", _BF16, shape, dev),
@@ -197,12 +197,12 @@ def rmsnorm_bwd(dY, H, weight, eps: float, dres=None, dH=None, dX=None, dW=None,
     w = _need(weight, "weight", (_BF16, _F32), (K,), dev)
     dr = _opt(dres, "dres", ht, shape, dev)
     if dH is None:
-        dH = _empty(shape, ht, dev, stream)
+        dH = _empty(dY, shape, ht, stream)
     if dW is None and want_dW:
-        dW = _empty((K,), _F32, dev, stream)
+        dW = _empty(dY, (K,), _F32, stream)
     if dW is not None and ws is None:
         need = _bytes(rmsnorm_workspace, dev, M, K)
-        ws = _empty((need,), torch.uint8, dev, stream) if need else None
+        ws = _empty(dY, (need,), torch.uint8, stream) if need else None
     _check(_library().qlora_rmsnorm_bwd(dy, h, _TYPE[ht], w, _TYPE[weight.dtype], eps, dr, M, K,
                                         _need(dH, "dH", ht, shape, dev), _opt(dX, "dX", _BF16, shape, dev),
                                         _opt(dW, "dW", _F32, (K,), dev), *_space(ws, dev), _raw(stream, dev)),
@@ -218,14 +218,16 @@ def _space(ws, dev):
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _adapter(act, act_name, w, w_name, act_shape, w_shape, dev):
-    """Addresses and rank of an optional adapter term: both factors or neither."""
+def _adapter(act, act_name, w, w_name, M, features, rank_first, dev):
+    """Addresses and rank of an optional adapter term, both factors or neither:
+    act [M, r] and w [features, r], or [r, features] with rank_first."""
     if act is None and w is None:
         return None, None, 0
     if act is None or w is None:
         raise ValueError(f"{act_name} and {w_name} go together")
     r = _matrix(act, act_name)[1]
-    return (_need(act, act_name, _BF16, act_shape(r), dev), _need(w, w_name, _BF16, w_shape(r), dev), r)
+    return (_need(act, act_name, _BF16, (M, r), dev),
+            _need(w, w_name, _BF16, (r, features) if rank_first else (features, r), dev), r)
 
 
 def i8_linear_fwd(W: I8Matrix, X: I8Matrix, sU=None, B=None, Y=None, status=None, stream=None):
@@ -235,9 +237,9 @@ def i8_linear_fwd(W: I8Matrix, X: I8Matrix, sU=None, B=None, Y=None, status=None
     dev = _device(X.codes, "X.codes")
     xq, sx = _need_i8(X, "X", xs, dev)
     wq, sw = _need_i8(W, "W", (N, K), dev)
-    u, b, r = _adapter(sU, "sU", B, "B", lambda r: (M, r), lambda r: (N, r), dev)
+    u, b, r = _adapter(sU, "sU", B, "B", M, N, False, dev)
     if Y is None:
-        Y = _empty((M, N), _BF16, dev, stream)
+        Y = _empty(X.codes, (M, N), _BF16, stream)
     _check(_library().qlora_i8_linear_fwd(xq, sx, M, wq, sw, N, K, u, b, r, _need(Y, "Y", _BF16, (M, N), dev),
                                           _opt(status, "status", torch.int32, (1,), dev), _raw(stream, dev)),
            "qlora_i8_linear_fwd")
@@ -257,11 +259,11 @@ def i8_linear_dx(W: I8Matrix, dY, sT=None, A=None, dX=None, ws=None, status=None
     dev = _device(dY, "dY")
     dy = _need(dY, "dY", _BF16, ys, dev)
     wq, sw = _need_i8(W, "W", (N, K), dev)
-    t, a, r = _adapter(sT, "sT", A, "A", lambda r: (M, r), lambda r: (r, K), dev)
+    t, a, r = _adapter(sT, "sT", A, "A", M, K, True, dev)
     if dX is None:
-        dX = _empty((M, K), _BF16, dev, stream)
+        dX = _empty(dY, (M, K), _BF16, stream)
     if ws is None:
-        ws = _empty((_bytes(i8_linear_workspace, dev, M, N, K),), torch.uint8, dev, stream)
+        ws = _empty(dY, (_bytes(i8_linear_workspace, dev, M, N, K),), torch.uint8, stream)
     _check(_library().qlora_i8_linear_dx(dy, M, wq, sw, N, K, t, a, r, _need(dX, "dX", _BF16, (M, K), dev),
                                          *_space(ws, dev), _opt(status, "status", torch.int32, (1,), dev),
                                          _raw(stream, dev)), "qlora_i8_linear_dx")
