@@ -456,11 +456,16 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
 // little more than one wave of pairs goes back to single tiles, two to a SM.
 // Measured (rank 16): 512 tokens 4096 x 4096 (128 tiles, 32 pair tiles) 12.9 us
 // split, 16.3 pair; 768 tokens (192, 48) 20.2 and 17.4; 200 tokens 11008 x 4096
-// (172, 43) 21.1 and 18.5; 384 tokens (258, 86) 23.0 and 29.5.
+// (172, 43) 21.1 and 18.5; 384 tokens (258, 86) 23.0 and 29.5. Past rank 16 the
+// single tiles' warp MMAs and fragment loads for the adapter cost more than the
+// pairs' tcgen05 term: 4096 tokens 432 x 192 rank 16 7.0 and 6.6 us, rank 32
+// 10.3 and 6.7, rank 64 22.1 and 6.8; 300 tokens 4096 x 1024 6.4 and 7.5, 8.8
+// and 7.6, 15.1 and 7.6; up to 128 tokens (100 of 1040 x 2064) 7.1 and 8.8, 7.7
+// and 8.8, 8.9 and 8.8.
 cudaError_t launch_i8_gemm(const I8GemmArgs &a, cudaStream_t st) {
   auto tiles = [&](int64_t t) { return ((a.F + t - 1) / t) * ((a.M + t - 1) / t); };
   const int64_t sms = device_sm_count(), single = tiles(128);
-  const bool split = single <= sms || (single <= 2 * sms && tiles(kTile) > sms / 2);
+  const bool split = (a.r <= 16 || a.M <= 128) && (single <= sms || (single <= 2 * sms && tiles(kTile) > sms / 2));
   return split ? launch_i8_split(a, st) : launch_i8_pair(a, st);
 }
 
