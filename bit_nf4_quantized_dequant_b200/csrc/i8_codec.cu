@@ -5,7 +5,10 @@
 //
 // Both are bound by memory (2 to 4 bytes read and 1 written an element), so a
 // row is read once and kept in registers, as it was loaded, between its maximum
-// and its codes.
+// and its codes. Measured: quantise 4096 x 14336 fp32 46 us (6.4 TB/s), 4096 x
+// 11008 bf16 26 us (5.2 TB/s), with column scales 33 us: there the scales' loads
+// from L1 and the instructions (67% of the issue slots) set the pace.
+// Dequantise 4096 x 4096 9 us (5.6 TB/s).
 #include "norm_i8.h"
 #include "row_device.cuh"
 

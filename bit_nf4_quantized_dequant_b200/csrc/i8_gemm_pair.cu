@@ -20,6 +20,12 @@
 // shares the tensor cores: 4096 tokens 14336 x 4096 took 152 us without an
 // adapter, 176 at rank 16 and 273 at rank 64.
 //
+// Bound by the tensor rate and, in long runs, by the board's power: 4096 tokens
+// 14336 x 4096 at rank 16 151 us before the cap (3.2 Pop/s, 97% of twice the
+// measured bf16 rate), 183 under it; 4096 x 4096 49 us (256 tiles, 3.5 turns of
+// 74 pairs). Below about 2048 codes of contraction the epilogue sets the pace:
+// 4096 x 1024 20 us without an adapter, 26 with one.
+//
 // Warps (384 threads): 0 TMA producer, 1 MMA issuer and TMEM owner, 2 adapter
 // producer, 4-11 epilogue (TMEM lane quadrant warp % 4, half of the columns
 // each).

