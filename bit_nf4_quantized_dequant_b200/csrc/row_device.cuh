@@ -104,9 +104,11 @@ __device__ __forceinline__ void load_cols(f2 (&f)[4], const void *p, int e, int 
     if constexpr (F32) {
       // 32 bytes a lane in one access where the address allows: two of 16 need twice the L1 wavefronts
       if (e < K && (reinterpret_cast<uintptr_t>(p) & 31u) == 0) {
-        asm("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
-            : "=l"(f[0]), "=l"(f[1]), "=l"(f[2]), "=l"(f[3])
-            : "l"(static_cast<const float *>(p) + e));
+        // volatile, with memory: else nothing keeps it behind grid_dep_wait, which the values may depend on
+        asm volatile("ld.global.v4.b64 {%0, %1, %2, %3}, [%4];"
+                     : "=l"(f[0]), "=l"(f[1]), "=l"(f[2]), "=l"(f[3])
+                     : "l"(static_cast<const float *>(p) + e)
+                     : "memory");
         return;
       }
     }

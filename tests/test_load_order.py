@@ -1,0 +1,46 @@
+"""Sources of the kernels that are launched before the work ahead of them has
+finished: what they read may still be written while they run, so every load has
+to stay behind the wait for that work. The compiler keeps that order only where
+the source states it; these tests read the sources (no GPU needed)."""
+
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "bit_nf4_quantized_dequant_b200", "csrc")
+EARLY = ["row_device.cuh", "i8_codec.cu", "rmsnorm.cu", "i8_gemm.cuh", "i8_gemm_split.cu", "i8_gemm_pair.cu"]
+
+
+def _code(name):
+    text = re.sub(r"/\*.*?\*/", "", open(os.path.join(CSRC, name)).read(), flags=re.S)
+    return re.sub(r"//[^\n]*", "", text)
+
+
+def _asm_statements(code):
+    """(is volatile, text) of every inline asm statement."""
+    for m in re.finditer(r"\basm\b\s*(volatile)?\s*\(", code):
+        depth, i, quoted = 1, m.end(), False
+        while depth:
+            c = code[i]
+            if c == '"' and code[i - 1] != "\\":
+                quoted = not quoted
+            elif not quoted:
+                depth += (c == "(") - (c == ")")
+            i += 1
+        yield m.group(1) is not None, code[m.end():i - 1]
+
+
+def test_the_list_names_every_early_kernel():
+    """A file that launches its kernels early is in EARLY (norm_i8.h declares the launch)."""
+    users = {f for f in os.listdir(CSRC) if f.endswith(".cu") and "launch_dependent(" in _code(f)}
+    assert users and users <= set(EARLY)
+
+
+@pytest.mark.parametrize("name", EARLY)
+def test_inline_loads_from_memory_state_their_order(name):
+    """An asm load that is neither volatile nor clobbers memory is a function of
+    its address to the compiler, free to move ahead of the wait."""
+    for volatile, text in _asm_statements(_code(name)):
+        if re.search(r'"[^"]*\b(ld|cp)\.', text):
+            assert volatile and re.search(r':\s*"memory"\s*$', text.strip()), text
