@@ -30,7 +30,7 @@ __device__ __forceinline__ void scaled(f2 (&f)[4], const Vec8<F32> &v, const f2 
 // and scaled by its columns (COLS), twice.
 template <int NV, bool WARP, bool ALIGNED, bool F32, bool COLS>
 __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 1 || NV == 8 ? 1 : (F32 ? 2 : 3)))
-    i8_quantize_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int K,
+    i8_quantize_kernel(const void *X, const float *col_scale, int64_t M, int K,
                        int8_t *__restrict__ codes, float *__restrict__ scale) {
   grid_dep_wait();
   grid_dep_launch();
@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 1 || 
 // Rows too long for registers: read twice (the second time mostly from L2).
 template <bool ALIGNED, bool F32, bool COLS>
 __global__ void __launch_bounds__(1024)
-    i8_quantize_long_kernel(const void *__restrict__ X, const float *__restrict__ col_scale, int64_t M, int K,
+    i8_quantize_long_kernel(const void *X, const float *col_scale, int64_t M, int K,
                             int8_t *__restrict__ codes, float *__restrict__ scale) {
   grid_dep_wait();
   grid_dep_launch();
@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(1024)
 // A block takes 1024 vectors of 8 codes of one row.
 template <bool ALIGNED>
 __global__ void __launch_bounds__(256)
-    i8_dequantize_rows_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int K, int blocks_a_row,
+    i8_dequantize_rows_kernel(const int8_t *codes, const float *scale, int K, int blocks_a_row,
                               uint16_t *__restrict__ out) {
   grid_dep_wait();
   grid_dep_launch();
@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(256)
 // Short rows: vectors of 8 codes over the whole matrix as one array; a vector
 // may cross into the next rows.
 __global__ void __launch_bounds__(256)
-    i8_dequantize_kernel(const int8_t *__restrict__ codes, const float *__restrict__ scale, int64_t M, int K,
+    i8_dequantize_kernel(const int8_t *codes, const float *scale, int64_t M, int K,
                          uint16_t *__restrict__ out) {
   grid_dep_wait();
   grid_dep_launch();

@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = sm.tmem_holder;
   grid_dep_launch();   // behind the allocation: a following kernel's CTAs do not take TMEM that this one still needs
-  grid_dep_wait();
+  const Waited after = grid_dep_wait();
 
   if (warp == 0) {
     // ---------------- producer: this CTA's tokens and features ----------------
@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t t_acc = t_warp + buf * kTile;
       float sx[4];   // tokens g, g + 8, g + 16, g + 24
 #pragma unroll
-      for (int i = 0; i < 4; ++i) sx[i] = m0 + g + 8 * i < p.M ? __ldg(p.act_scale + m0 + g + 8 * i) : 0.f;
+      for (int i = 0; i < 4; ++i) sx[i] = m0 + g + 8 * i < p.M ? load_after(after, p.act_scale + m0 + g + 8 * i) : 0.f;
       float2 sw[4][4];   // the features of this warp's chunks
       if constexpr (!kDx) {
 #pragma unroll
@@ -303,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int64_t f = f0 + (half + 2 * i) * 32 + j * 8 + q2;
-            sw[i][j] = f < p.F ? __ldg(reinterpret_cast<const float2 *>(p.w_scale + f)) : make_float2(0.f, 0.f);
+            sw[i][j] = f < p.F ? load_after(after, reinterpret_cast<const float2 *>(p.w_scale + f)) : make_float2(0.f, 0.f);
           }
       }
       if (!__all_sync(0xffffffffu, mbar_wait(&sm.accf[buf], (n >> 1) & 1u, abort_flag, p.status))) {

@@ -73,21 +73,21 @@ struct BlockOperands {
   uint32_t u[kSteps ? kSteps : 1][4];
   uint32_t b[kSteps ? kSteps : 1][2][2];
 
-  __device__ __forceinline__ void load(const SplitParams &p, int64_t m0, int64_t f0, int lane) {
+  __device__ __forceinline__ void load(Waited after, const SplitParams &p, int64_t m0, int64_t f0, int lane) {
     const int g = lane >> 2, q2 = (lane & 3) * 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int64_t m = m0 + g + 8 * i, f = f0 + 8 * i + q2;
-      sx[i] = m < p.M ? __ldg(p.act_scale + m) : 0.f;
+      sx[i] = m < p.M ? load_after(after, p.act_scale + m) : 0.f;
       sw[i] = make_float2(1.f, 1.f);
-      if (!kDx && f < p.F) sw[i] = __ldg(reinterpret_cast<const float2 *>(p.w_scale + f));
+      if (!kDx && f < p.F) sw[i] = load_after(after, reinterpret_cast<const float2 *>(p.w_scale + f));
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const int k = ks * 16 + c * 8 + q2;
-          u[ks][i + 2 * c] = lora_act_pair(p.lora_act, p.M, p.r, m, k);
-          b[ks][i][c] = lora_w_pair<kDx>(p.lora_w, p.F, p.r, f0 + 8 * i + g, k);
+          u[ks][i + 2 * c] = lora_act_pair(after, p.lora_act, p.M, p.r, m, k);
+          b[ks][i][c] = lora_w_pair<kDx>(after, p.lora_w, p.F, p.r, f0 + 8 * i + g, k);
         }
     }
   }
@@ -156,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   grid_dep_launch();   // behind the allocation: a following kernel's CTAs do not take TMEM that this one still needs
-  grid_dep_wait();
+  const Waited after = grid_dep_wait();
 
   if (warp == 0) {
     if (elect_one()) {
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // blocks (row of blocks rb, column of blocks cb) that hold tokens, dealt out to the cluster's warps
     const int blocks = (tokens + 15) / 16 * 8, step = split * (kThreads / 32);
     int b = warp * split + rank;
-    if (b < blocks) op.load(p, t0 + (b >> 3) * 16, f0 + (b & 7) * 16, lane);   // under the main loop
+    if (b < blocks) op.load(after, p, t0 + (b >> 3) * 16, f0 + (b & 7) * 16, lane);   // under the main loop
     int4 *part = reinterpret_cast<int4 *>(ring);   // [block][2][lane]
     // the TMEM loads are warp-wide: every lane takes the same way
     if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.status))) {
@@ -260,13 +260,13 @@ __global__ void __launch_bounds__(kThreads, 2)
             s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
           }
         op.finish(p, t0 + (b >> 3) * 16, f0 + (b & 7) * 16, lane, s);
-        if (b + step < blocks) op.load(p, t0 + ((b + step) >> 3) * 16, f0 + ((b + step) & 7) * 16, lane);
+        if (b + step < blocks) op.load(after, p, t0 + ((b + step) >> 3) * 16, f0 + ((b + step) & 7) * 16, lane);
       }
     }
     // no CTA leaves while a peer may still read its partial sums
     cluster_sync_all();
   } else {
-    if (quad * 32 < tokens) op.load(p, t0 + quad * 32, f0 + half * 64, lane);   // under the main loop
+    if (quad * 32 < tokens) op.load(after, p, t0 + quad * 32, f0 + half * 64, lane);   // under the main loop
     if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.status))) {
       tc_fence_after();
 #pragma unroll 1
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           int s[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[e] = static_cast<int>(v[8 * c + e]);
-          if (h || c) op.load(p, m0, f0 + half * 64 + c * 16, lane);
+          if (h || c) op.load(after, p, m0, f0 + half * 64 + c * 16, lane);
           op.finish(p, m0, f0 + half * 64 + c * 16, lane, s);
         }
       }

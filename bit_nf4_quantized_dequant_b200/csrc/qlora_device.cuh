@@ -69,7 +69,39 @@ __device__ __forceinline__ bool elect_one() {
 // ahead of it on the stream has finished; grid_dep_wait returns once that work
 // is complete and its writes are visible. grid_dep_launch lets the next such
 // kernel start once every CTA of this one has called it or left.
-__device__ __forceinline__ void grid_dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// What such a kernel reads may be written while it runs, so none of it may come
+// by the read-only path (__ldg, const __restrict__), and no load may move ahead of
+// the wait. Plain loads stay behind it. Where those would also be held behind the
+// kernel's own stores, load_after takes the order from its first argument alone:
+// the wait's result, without which the load cannot be issued.
+struct Waited {
+  uint32_t order;
+};
+__device__ __forceinline__ Waited grid_dep_wait() {
+  Waited w;
+  asm volatile("griddepcontrol.wait;\n\tmov.u32 %0, 0;" : "=r"(w.order)::"memory");
+  return w;
+}
+__device__ __forceinline__ uint16_t load_after(Waited w, const uint16_t *p) {
+  uint16_t v;
+  asm("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p), "r"(w.order));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_after(Waited w, const uint32_t *p) {
+  uint32_t v;
+  asm("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p), "r"(w.order));
+  return v;
+}
+__device__ __forceinline__ float load_after(Waited w, const float *p) {
+  float v;
+  asm("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p), "r"(w.order));
+  return v;
+}
+__device__ __forceinline__ float2 load_after(Waited w, const float2 *p) {
+  float2 v;
+  asm("ld.global.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "l"(p), "r"(w.order));
+  return v;
+}
 __device__ __forceinline__ void grid_dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Record the first device-side error of a call (never clears an earlier one).

@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(256)
 // partials: 19.5 us with 32, 18.4 with 8; 4096 x 4096, 296 partials: 26.8 and 29.0).
 template <int COLS>
 __global__ void __launch_bounds__(1024)
-    rmsnorm_dw_kernel(const float *__restrict__ part, int rows, int64_t K, float *__restrict__ dw) {
+    rmsnorm_dw_kernel(const float *part, int rows, int64_t K, float *__restrict__ dw) {
   grid_dep_wait();
   grid_dep_launch();
   constexpr int G = 1024 / COLS;

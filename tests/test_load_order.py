@@ -37,10 +37,22 @@ def test_the_list_names_every_early_kernel():
     assert users and users <= set(EARLY)
 
 
-@pytest.mark.parametrize("name", EARLY)
+@pytest.mark.parametrize("name", EARLY + ["qlora_device.cuh"])
 def test_inline_loads_from_memory_state_their_order(name):
     """An asm load that is neither volatile nor clobbers memory is a function of
-    its address to the compiler, free to move ahead of the wait."""
+    its operands to the compiler, free to move ahead of the wait unless the
+    wait's result is one of them."""
     for volatile, text in _asm_statements(_code(name)):
         if re.search(r'"[^"]*\b(ld|cp)\.', text):
-            assert volatile and re.search(r':\s*"memory"\s*$', text.strip()), text
+            ordered = volatile and re.search(r':\s*"memory"\s*$', text.strip())
+            assert ordered or '"r"(w.order)' in text, text
+
+
+@pytest.mark.parametrize("name", EARLY)
+def test_no_load_by_the_read_only_path(name):
+    """That path is for memory that nothing writes while the kernel runs: the
+    launch ahead may still be writing a scale, an activation or a partial sum.
+    const __restrict__ lets the compiler take it by itself."""
+    code = _code(name)
+    assert not re.findall(r"__ldg\s*\([^;]*|ld\.global\.nc[^;]*", code)
+    assert not re.findall(r"\bconst\s+\w+\s*\*\s*__restrict__\s*\w+", code)
