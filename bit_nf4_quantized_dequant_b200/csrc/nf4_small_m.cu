@@ -756,7 +756,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) nf4_small_m_kernel(const __grid
     // ======================= epilogue =======================
     const int et = threadIdx.x - kEpiWarp0 * 32;   // 0..127: a tile row
     const int ew = et >> 5;
-    if (P.pdl) grid_dep_wait();
+    Waited after{0};   // activations and adapters may come from the preceding launch
+    if (P.pdl) after = grid_dep_wait();
 
     // ---- pieces of X A^T: 128 K each, every load issued before the MMAs ----
     // Inside each 64-K block the K order is permuted as in the weight path: lane
@@ -781,8 +782,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) nf4_small_m_kernel(const __grid
           const int t = 8 * u + g;
           const uint4 *xr = reinterpret_cast<const uint4 *>(q.X + static_cast<int64_t>(t) * q.K + k0 + 64 * bl + 16 * c);
           const bool ok = t < P.M && (bl == 0 || two);
-          xv[bl][u][0] = ok ? __ldg(xr) : make_uint4(0, 0, 0, 0);
-          xv[bl][u][1] = ok ? __ldg(xr + 1) : make_uint4(0, 0, 0, 0);
+          xv[bl][u][0] = ok ? load_after(after, xr) : make_uint4(0, 0, 0, 0);
+          xv[bl][u][1] = ok ? load_after(after, xr + 1) : make_uint4(0, 0, 0, 0);
         }
       float d[4][NT][4];
 #pragma unroll
@@ -798,8 +799,8 @@ __global__ void __launch_bounds__(kSmThreads, 1) nf4_small_m_kernel(const __grid
               const int j = 16 * jt + g + 8 * h;
               const uint4 *ar = reinterpret_cast<const uint4 *>(q.A + static_cast<int64_t>(j) * q.K + k0 + 64 * bl + 16 * c);
               const bool ok = j < q.r && (bl == 0 || two);
-              av[bl][h][0] = ok ? __ldg(ar) : make_uint4(0, 0, 0, 0);
-              av[bl][h][1] = ok ? __ldg(ar + 1) : make_uint4(0, 0, 0, 0);
+              av[bl][h][0] = ok ? load_after(after, ar) : make_uint4(0, 0, 0, 0);
+              av[bl][h][1] = ok ? load_after(after, ar + 1) : make_uint4(0, 0, 0, 0);
             }
 #pragma unroll
           for (int bl = 0; bl < 2; ++bl)
@@ -905,7 +906,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) nf4_small_m_kernel(const __grid
         if (n < q.N) {
 #pragma unroll
           for (int j8 = 0; j8 < BPRE; ++j8)
-            if (j8 < q.r / 8) bpre[j8] = __ldg(brow + j8);
+            if (j8 < q.r / 8) bpre[j8] = load_after(after, brow + j8);
         }
       }
       const int eb = seg_idx & 1;
@@ -992,7 +993,7 @@ __global__ void __launch_bounds__(kSmThreads, 1) nf4_small_m_kernel(const __grid
 #pragma unroll
         for (int j8 = 0; j8 < 8; ++j8) {
           if (j8 < q.r / 8) {
-            const uint4 bv = j8 < BPRE ? bpre[j8 < BPRE ? j8 : 0] : __ldg(brow + j8);
+            const uint4 bv = j8 < BPRE ? bpre[j8 < BPRE ? j8 : 0] : load_after(after, brow + j8);
             const uint32_t bw[4] = {bv.x, bv.y, bv.z, bv.w};
             float bj[8];
 #pragma unroll

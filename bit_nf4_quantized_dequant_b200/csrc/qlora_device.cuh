@@ -92,6 +92,11 @@ __device__ __forceinline__ uint32_t load_after(Waited w, const uint32_t *p) {
   asm("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p), "r"(w.order));
   return v;
 }
+__device__ __forceinline__ uint4 load_after(Waited w, const uint4 *p) {
+  uint4 v;
+  asm("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p), "r"(w.order));
+  return v;
+}
 __device__ __forceinline__ float load_after(Waited w, const float *p) {
   float v;
   asm("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p), "r"(w.order));

@@ -56,3 +56,12 @@ def test_no_load_by_the_read_only_path(name):
     code = _code(name)
     assert not re.findall(r"__ldg\s*\([^;]*|ld\.global\.nc[^;]*", code)
     assert not re.findall(r"\bconst\s+\w+\s*\*\s*__restrict__\s*\w+", code)
+
+
+def test_few_token_forward_reads_only_weights_by_the_read_only_path():
+    """Its overlap flag promises that the NF4 weights are not written by the work
+    ahead; activations and adapters may be."""
+    code = _code("nf4_small_m.cu")
+    assert "grid_dep_wait" in code
+    reads = re.findall(r"__ldg\s*\(([^;]*?)\)", code)
+    assert reads and all(re.match(r"q\.(scale8|scale2|codes)\b", r) for r in reads), reads
