@@ -29,10 +29,13 @@ qlora_status_t check_rows(int64_t M, int64_t K, int64_t most) {
   return QLORA_OK;
 }
 
-// The shapes and adapter of both products; C is the contraction's length.
-qlora_status_t check_i8_shape(int64_t M, int64_t N, int64_t K, int32_t r) {
+// The shapes and adapter of both products. Only the dimension that is summed over
+// has a limit of its own: K in the forward, N in the gradient (whose rows of N the
+// codec also quantises, the lower limit of the two).
+qlora_status_t check_i8_shape(bool dx, int64_t M, int64_t N, int64_t K, int32_t r) {
   if (M < 1 || N < 1 || K < 1) return QLORA_ERR_INVALID_ARG;
-  if (N % 16 || K % 16 || M > kMaxLinear || N > kMaxLinear || K > kMaxContraction) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (N % 16 || K % 16 || M > kMaxLinear) return QLORA_ERR_UNSUPPORTED_SHAPE;
+  if (N > (dx ? kMaxQuantCols : kMaxLinear) || K > (dx ? kMaxLinear : kMaxContraction)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   if (r != 0 && (r < 8 || r > 64 || r % 8)) return QLORA_ERR_UNSUPPORTED_SHAPE;
   return QLORA_OK;
 }
@@ -100,7 +103,7 @@ qlora_status_t qlora_i8_linear_fwd(const int8_t *Xq, const float *sx, int64_t M,
                                    int64_t N, int64_t K, const uint16_t *sU, const uint16_t *B, int32_t r, uint16_t *Y,
                                    int32_t *dev_status, qlora_stream_t stream) {
   if (!Xq || !sx || !Wq || !sw || !Y) return QLORA_ERR_INVALID_ARG;
-  const qlora_status_t st = check_i8_shape(M, N, K, r);
+  const qlora_status_t st = check_i8_shape(false, M, N, K, r);
   if (st != QLORA_OK) return st;
   if (r && (!sU || !B)) return QLORA_ERR_INVALID_ARG;
   if (!all_aligned16(Xq, sx, Wq, sw, Y) || (r && !all_aligned16(sU, B))) return QLORA_ERR_MISALIGNED;
@@ -123,9 +126,8 @@ qlora_status_t qlora_i8_linear_fwd(const int8_t *Xq, const float *sx, int64_t M,
 
 qlora_status_t qlora_i8_linear_workspace(int64_t M, int64_t N, int64_t K, size_t *bytes) {
   if (!bytes) return QLORA_ERR_INVALID_ARG;
-  const qlora_status_t st = check_i8_shape(M, N, K, 0);
+  const qlora_status_t st = check_i8_shape(true, M, N, K, 0);
   if (st != QLORA_OK) return st;
-  if (N > kMaxQuantCols) return QLORA_ERR_UNSUPPORTED_SHAPE;
   *bytes = round_up(static_cast<size_t>(M) * N, 256) + static_cast<size_t>(M) * 4;
   return QLORA_OK;
 }
@@ -134,7 +136,7 @@ qlora_status_t qlora_i8_linear_dx(const uint16_t *dY, int64_t M, const int8_t *W
                                   int64_t K, const uint16_t *sT, const uint16_t *A, int32_t r, uint16_t *dX, void *ws,
                                   size_t ws_bytes, int32_t *dev_status, qlora_stream_t stream) {
   if (!dY || !Wq || !sw || !dX) return QLORA_ERR_INVALID_ARG;
-  qlora_status_t st = check_i8_shape(M, N, K, r);
+  qlora_status_t st = check_i8_shape(true, M, N, K, r);
   if (st != QLORA_OK) return st;
   if (r && (!sT || !A)) return QLORA_ERR_INVALID_ARG;
   if (!all_aligned16(dY, Wq, sw, dX) || (r && !all_aligned16(sT, A))) return QLORA_ERR_MISALIGNED;

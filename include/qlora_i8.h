@@ -109,7 +109,8 @@ qlora_status_t qlora_i8_linear_workspace(int64_t M, int64_t N, int64_t K, size_t
  *   dX[m, k] = bf16_rn(fp32(sum_n gq[m, n] Wq[n, k]) sg[m] + sum_j sT[m, j] A[j, k])
  * dY [M, N] bf16; sT [M, r] and A [r, K] bf16 as in qlora_fused_dx, or r = 0.
  * dX [M, K] bf16. The adapter's gradients are qlora_lora_grads as for the NF4
- * linear. M >= 1, N % 16 == 0, K % 16 == 0, N <= 65536.
+ * linear. M >= 1, N % 16 == 0, K % 16 == 0, N <= 65536; K, which is not summed
+ * over, may pass the forward's limit.
  * Errors: as qlora_i8_linear_fwd, and WORKSPACE. */
 qlora_status_t qlora_i8_linear_dx(const uint16_t *dY, int64_t M, const int8_t *Wq, const float *sw, int64_t N,
                                   int64_t K, const uint16_t *sT, const uint16_t *A, int32_t r, uint16_t *dX,

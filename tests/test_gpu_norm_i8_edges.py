@@ -1,0 +1,37 @@
+"""The RMS norm and the 8-bit linear at the edges of what their header allows."""
+
+import numpy as np
+import pytest
+
+from oracle import i8 as oi8
+
+pytestmark = pytest.mark.gpu
+
+EPS = 1e-5
+U32, U16 = 2.0 ** -24, 2.0 ** -8
+
+
+def _f64(t):
+    return t.double().cpu().numpy()
+
+
+@pytest.mark.parametrize("M,N,r", [(3, 48, 0), (140, 16, 16), (300, 48, 40)])
+def test_gradient_wider_than_the_longest_contraction(lib, M, N, r):
+    """K = 131088 features: the gradient sums over N alone. Off by three fp32
+    roundings of the scaled sum, r + 1 of the adapter's on the magnitudes, and bf16's."""
+    import torch
+    K = 131072 + 16
+    g = np.random.default_rng(M)
+    wq = g.integers(-127, 128, (N, K), dtype=np.int8)
+    sw = (0.5 + g.random(N)).astype(np.float32) * 1e-3
+    bf = lambda s, *shape: torch.from_numpy((g.standard_normal(shape) * s).astype(np.float32)).bfloat16()
+    dy, t, a = bf(1.0, M, N), bf(0.1, M, r), bf(0.05, r, K)
+    W = lib.I8Matrix(torch.from_numpy(wq).cuda(), torch.from_numpy(sw).cuda())
+    args = dict(sT=t.cuda(), A=a.cuda()) if r else {}
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    dX = lib.i8_linear_dx(W, dy.cuda(), status=status, **args)
+    main = oi8.linear_dx(dy.float().numpy(), wq, sw)
+    term, mag = (_f64(t) @ _f64(a), np.abs(_f64(t)) @ np.abs(_f64(a))) if r else (0.0, 0.0)
+    ref, tol = main + term, (r + 5) * U32 * (np.abs(main) + mag)
+    assert status.item() == 0
+    assert np.all(np.abs(_f64(dX) - ref) <= tol + U16 * (np.abs(ref) + tol) + 1e-38)
