@@ -68,6 +68,7 @@ qlora_status_t qlora_rmsnorm_fwd(const uint16_t *X, const void *R, int32_t h_typ
   if ((!X && !R) || !weight || !type_ok(h_type) || !type_ok(w_type)) return QLORA_ERR_INVALID_ARG;
   if (!R && h_type != QLORA_TYPE_BF16) return QLORA_ERR_INVALID_ARG;
   if ((!Y && !codes) || !codes != !scale) return QLORA_ERR_INVALID_ARG;
+  if (Y && H == Y) return QLORA_ERR_INVALID_ARG;   // both outputs in one buffer
   if (!std::isfinite(eps) || eps < 0.f) return QLORA_ERR_INVALID_ARG;
   const qlora_status_t st = check_rows(M, K, kMaxNormCols);
   if (st != QLORA_OK) return st;

@@ -52,9 +52,10 @@ qlora_status_t qlora_i8_dequantize(const int8_t *codes, const float *scale, int6
  * weight [K] of w_type. eps >= 0, finite.
  * Outputs, each optional, at least one of Y and codes: H [M, K] of h_type (may
  *   be R, or X where h_type is bf16: every element is read before it is
- *   written); Y [M, K] = bf16_rn(y) (may be X); codes [M, K] and scale [M] (both
- *   or neither) = the int8 rows of y as qlora_i8_quantize would give them for
- *   the fp32 y (y is not rounded to bf16 first).
+ *   written); Y [M, K] = bf16_rn(y) (may be X where H is not: H and Y in one
+ *   buffer are refused); codes [M, K] and scale [M] (both or neither) = the int8
+ *   rows of y as qlora_i8_quantize would give them for the fp32 y (y is not
+ *   rounded to bf16 first).
  * M >= 1, 1 <= K <= 32768. Errors: INVALID_ARG, UNSUPPORTED_SHAPE, MISALIGNED, CUDA. */
 qlora_status_t qlora_rmsnorm_fwd(const uint16_t *X, const void *R, int32_t h_type, const void *weight,
                                  int32_t w_type, float eps, int64_t M, int64_t K, void *H, uint16_t *Y,

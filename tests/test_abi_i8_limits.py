@@ -28,3 +28,12 @@ def test_the_gradient_sums_over_n_alone(so):
     assert ws(4, 64, 1 << 31) == dx(64, 1 << 31) == ws(1 << 31, 64, 64) == dx(64, 64, 1 << 31) == SHAPE
     assert ws(4, 65536, 64) == OK and ws(4, 65552, 64) == dx(65552, 64) == SHAPE
     assert so.qlora_i8_linear_fwd(X, S, 4, W, T, 64, 131072, None, None, 0, Y, None, None) == SHAPE
+
+
+def test_stream_and_norm_in_one_buffer_are_refused(so):
+    """H may be X and Y may be X, but not both in one call: one would overwrite
+    the other."""
+    # a call that gets past its pointers ends at its K, which is too large
+    g = lambda x=X, r=V, h=T, y=Y: so.qlora_rmsnorm_fwd(x, r, 0, W, 0, 1e-5, 4, 32769, h, y, None, None, None)
+    assert g() == g(h=X) == g(y=X) == g(h=V, y=X) == g(h=None) == SHAPE
+    assert g(h=X, y=X) == g(h=T, y=T) == g(h=V, y=V) == INVALID
