@@ -186,9 +186,10 @@ def rmsnorm_workspace(M: int, K: int) -> int:
 
 
 def rmsnorm_bwd(dY, H, weight, eps: float, dres=None, dH=None, dX=None, dW=None, ws=None, want_dW: bool = True,
-                stream=None):
-    """(dH, dX, dW): the gradient of the stream h in its type, its bf16 copy
-    (only when dX is passed) and the weight's (fp32, or None without want_dW)."""
+                stream=None, want_dH: bool = True):
+    """(dH, dX, dW): the gradient of the stream h in its type (None without
+    want_dH, for a first block's norm with dX passed), its bf16 copy (only when
+    dX is passed) and the weight's (fp32, or None without want_dW)."""
     M, K = shape = _matrix(dY, "dY")
     dev = _device(dY, "dY")
     ht = H.dtype
@@ -196,7 +197,7 @@ def rmsnorm_bwd(dY, H, weight, eps: float, dres=None, dH=None, dX=None, dW=None,
     h = _need(H, "H", (_BF16, _F32), shape, dev)
     w = _need(weight, "weight", (_BF16, _F32), (K,), dev)
     dr = _opt(dres, "dres", ht, shape, dev)
-    if dH is None:
+    if dH is None and want_dH:
         dH = _empty(dY, shape, ht, stream)
     if dW is None and want_dW:
         dW = _empty(dY, (K,), _F32, stream)
@@ -204,7 +205,7 @@ def rmsnorm_bwd(dY, H, weight, eps: float, dres=None, dH=None, dX=None, dW=None,
         need = _bytes(rmsnorm_workspace, dev, M, K)
         ws = _empty(dY, (need,), torch.uint8, stream) if need else None
     _check(_library().qlora_rmsnorm_bwd(dy, h, _TYPE[ht], w, _TYPE[weight.dtype], eps, dr, M, K,
-                                        _need(dH, "dH", ht, shape, dev), _opt(dX, "dX", _BF16, shape, dev),
+                                        _opt(dH, "dH", ht, shape, dev), _opt(dX, "dX", _BF16, shape, dev),
                                         _opt(dW, "dW", _F32, (K,), dev), *_space(ws, dev), _raw(stream, dev)),
            "qlora_rmsnorm_bwd")
     return dH, dX, dW

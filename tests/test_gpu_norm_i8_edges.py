@@ -35,3 +35,17 @@ def test_gradient_wider_than_the_longest_contraction(lib, M, N, r):
     ref, tol = main + term, (r + 5) * U32 * (np.abs(main) + mag)
     assert status.item() == 0
     assert np.all(np.abs(_f64(dX) - ref) <= tol + U16 * (np.abs(ref) + tol) + 1e-38)
+
+
+@pytest.mark.parametrize("M,K", [(4, 264), (300, 1001), (40, 2048), (3, 16392)])
+def test_bf16_copy_without_the_stream_gradient(lib, M, K):
+    """want_dH=False: no dH is allocated or written, the other outputs are the same."""
+    import torch
+    g = torch.Generator().manual_seed(M)
+    dy, h = torch.randn(M, K, generator=g).bfloat16().cuda(), torch.randn(M, K, generator=g).cuda()
+    w = (1 + 0.1 * torch.randn(K, generator=g)).cuda()
+    _, dX, dW = lib.rmsnorm_bwd(dy, h, w, EPS, dX=torch.empty_like(dy))
+    none, dX1, dW1 = lib.rmsnorm_bwd(dy, h, w, EPS, dX=torch.empty_like(dy), want_dH=False)
+    assert none is None and torch.equal(dX, dX1) and torch.equal(dW, dW1)
+    with pytest.raises(lib.QloraError, match="INVALID_ARG"):
+        lib.rmsnorm_bwd(dy, h, w, EPS, want_dH=False)
