@@ -125,6 +125,7 @@ __device__ __forceinline__ void drain_slot(uint64_t *full, uint32_t parity) {
   }
 }
 
+int i8_split_ways(int64_t M, int64_t F, int64_t C);                  // how many CTAs the split kernel gives a tile
 cudaError_t launch_i8_split(const I8GemmArgs &a, cudaStream_t st);   // i8_gemm_split.cu
 cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st);    // i8_gemm_pair.cu
 cudaError_t launch_i8_gemm(const I8GemmArgs &a, cudaStream_t st);    // the one of the two that fits the sizes

@@ -462,16 +462,31 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
 // little more than one wave of pairs goes back to single tiles, two to a SM.
 // Measured (rank 16): 512 tokens 4096 x 4096 (128 tiles, 32 pair tiles) 12.9 us
 // split, 16.3 pair; 768 tokens (192, 48) 20.2 and 17.4; 200 tokens 11008 x 4096
-// (172, 43) 21.1 and 18.5; 384 tokens (258, 86) 23.0 and 29.5. Past rank 16 the
-// single tiles' warp MMAs and fragment loads for the adapter cost more than the
-// pairs' tcgen05 term: 4096 tokens 432 x 192 rank 16 7.0 and 6.6 us, rank 32
-// 10.3 and 6.7, rank 64 22.1 and 6.8; 300 tokens 4096 x 1024 6.4 and 7.5, 8.8
-// and 7.6, 15.1 and 7.6; up to 128 tokens (100 of 1040 x 2064) 7.1 and 8.8, 7.7
-// and 8.8, 8.9 and 8.8.
+// (172, 43) 21.1 and 18.5; 384 tokens (258, 86) 23.0 and 29.5.
+//
+// Past rank 16 the single tiles' warp MMAs and fragment loads for the adapter cost
+// more than the pairs' tcgen05 term: 0.35 us (gradient: 0.60) for each further 16
+// ranks and block of 16 x 16 that a warp finishes, 8 / split of them. The pairs
+// in turn do a tile's whole contraction in one place, at 0.13 us (0.32) a step
+// where few tiles are at work, the CTAs of a cluster their part at 0.25 us. Rank
+// 32, split and pair: 4096 tokens 432 x 192 (one way, 2 steps) 9.8 and 6.7 us,
+// 300 tokens 4096 x 1024 (one, 8) 8.5 and 7.5, 1024 tokens 1024 x 4096 (two, 32)
+// 10.8 and 10.1, 256 tokens 1024 x 4096 (eight, 32) 8.3 and 9.3, 256 tokens
+// 1024 x 14336 (eight, 112) 10.9 and 19.8; gradient 10.9 and 10.0, 13.1 and 12.2,
+// 18.0 and 21.5, 11.7 and 17.5, 17.9 and 43.6; at rank 64 of 1024 tokens 14.4 and
+// 10.1, gradient 24.1 and 21.6. Up to 128 tokens half of a pair's tile is empty:
+// 100 of 1040 x 2064 at rank 16, 32 and 64 7.1, 7.7 and 8.9 us split, 8.8 pair.
+bool adapter_fits_split(const I8GemmArgs &a) {
+  if (a.r <= 16 || a.M <= 128) return true;
+  const int64_t nk = (a.C + kI8Step - 1) / kI8Step, ways = i8_split_ways(a.M, a.F, a.C);
+  const int64_t adapter = (a.dx ? 60 : 35) * ((8 + ways - 1) / ways) * ((a.r + 15) / 16 - 1);   // in 10 ns
+  return adapter <= (a.dx ? 32 : 13) * nk - 25 * ((nk + ways - 1) / ways);
+}
+
 cudaError_t launch_i8_gemm(const I8GemmArgs &a, cudaStream_t st) {
   auto tiles = [&](int64_t t) { return ((a.F + t - 1) / t) * ((a.M + t - 1) / t); };
   const int64_t sms = device_sm_count(), single = tiles(128);
-  const bool split = (a.r <= 16 || a.M <= 128) && (single <= sms || (single <= 2 * sms && tiles(kTile) > sms / 2));
+  const bool split = (single <= sms || (single <= 2 * sms && tiles(kTile) > sms / 2)) && adapter_fits_split(a);
   return split ? launch_i8_split(a, st) : launch_i8_pair(a, st);
 }
 

@@ -339,6 +339,17 @@ static int resident_clusters(int split) {
   return n;
 }
 
+// As many CTAs as there are SMs, each with about four steps or more. Measured
+// with one token of 4096 x 4096 (32 tiles of 32 steps): 4 ways 6.3 us, 3 ways
+// 6.7, 2 ways 7.2, 8 ways (two CTAs a SM) 7.2; 1024 x 4096: 8 ways 5.1, 4 ways 5.9.
+// A cluster stays inside one GPC, which leaves some SMs out: see resident_clusters.
+int i8_split_ways(int64_t M, int64_t F, int64_t C) {
+  const int64_t tiles = ((F + kTile - 1) / kTile) * ((M + kTile - 1) / kTile), nk = (C + kI8Step - 1) / kI8Step;
+  int split = static_cast<int>((nk + 3) / 4 < kMaxSplit ? (nk + 3) / 4 : kMaxSplit);
+  while (split > 1 && tiles > resident_clusters(split)) --split;
+  return split;
+}
+
 cudaError_t launch_i8_split(const I8GemmArgs &a, cudaStream_t st) {
   SplitParams p{};
   p.act_scale = a.act_scale;
@@ -354,12 +365,7 @@ cudaError_t launch_i8_split(const I8GemmArgs &a, cudaStream_t st) {
   p.nk = static_cast<int>((a.C + kI8Step - 1) / kI8Step);
   p.feat_tiles = static_cast<int>((a.F + kTile - 1) / kTile);
   const int64_t tiles = static_cast<int64_t>(p.feat_tiles) * ((a.M + kTile - 1) / kTile);
-  // As many CTAs as there are SMs, each with about four steps or more. Measured
-  // with one token of 4096 x 4096 (32 tiles of 32 steps): 4 ways 6.3 us, 3 ways
-  // 6.7, 2 ways 7.2, 8 ways (two CTAs a SM) 7.2; 1024 x 4096: 8 ways 5.1, 4 ways 5.9.
-  // A cluster stays inside one GPC, which leaves some SMs out: see resident_clusters.
-  p.split = (p.nk + 3) / 4 < kMaxSplit ? (p.nk + 3) / 4 : kMaxSplit;
-  while (p.split > 1 && tiles > resident_clusters(p.split)) --p.split;
+  p.split = i8_split_ways(a.M, a.F, a.C);
   const int per_cta = (p.nk + p.split - 1) / p.split;
   // two CTAs a SM where there are more than SMs, else one with a deeper ring
   const uint32_t room = (tiles * p.split > device_sm_count() ? 108u : 200u) * 1024u;
