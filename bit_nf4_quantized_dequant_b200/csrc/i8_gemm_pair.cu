@@ -21,10 +21,11 @@
 // adapter, 176 at rank 16 and 273 at rank 64.
 //
 // Bound by the tensor rate and, in long runs, by the board's power: 4096 tokens
-// 14336 x 4096 at rank 16 151 us before the cap (3.2 Pop/s, 97% of twice the
-// measured bf16 rate), 183 under it; 4096 x 4096 49 us (256 tiles, 3.5 turns of
-// 74 pairs). Below about 2048 codes of contraction the epilogue sets the pace:
-// 4096 x 1024 20 us without an adapter, 26 with one.
+// 14336 x 4096 at rank 16 takes 152 to 154 us in bursts of five calls after a pause
+// (3.1 Pop/s, 95% of twice the measured bf16 rate), 175 to 181 in a long run under
+// the cap; 4096 x 4096 49 us (256 tiles, 3.5 turns of 74 pairs). Below about 2048
+// codes of contraction the epilogue sets the pace: 4096 x 1024 19 us without an
+// adapter, 26 with one, and a third more on a board that is at its cap.
 //
 // Warps (384 threads): 0 TMA producer, 1 MMA issuer and TMEM owner, 2 adapter
 // producer, 4-11 epilogue (TMEM lane quadrant warp % 4, half of the columns

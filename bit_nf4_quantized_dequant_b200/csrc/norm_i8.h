@@ -15,9 +15,12 @@ cudaError_t allow_smem(void (*kernel)(P...), int most = 220 * 1024) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
 }
 
-// Launches a kernel that begins with grid_dep_wait, so that its launch and set-up
-// overlap the end of the work ahead of it on the stream (about 2 us of a call
-// among others). cluster: CTAs of a cluster.
+// Launches a kernel that reads and writes nothing before grid_dep_wait, so that its
+// launch and set-up overlap the end of the work ahead of it on the stream. It saves
+// 0.4 to 1.4 us a call in a graph (norm 8 x 4096 1.6 and 2.2 us, one token of
+// 14336 x 4096 12.3 and 13.5; norm gradient 8192 x 1024 18.0 and 17.9: nothing) and
+// 0.3 to 5.6 us a call launched among others (4096 x 4096 norm 21.7 and 24.4 us, its
+// gradient's two launches 27.3 and 32.8). cluster: CTAs of a cluster.
 template <class... P, class... A>
 cudaError_t launch_dependent(void (*kernel)(P...), unsigned grid, int threads, size_t smem, cudaStream_t st, int cluster,
                              const A &...args) {

@@ -29,9 +29,12 @@ __device__ __forceinline__ float inv_rms(float sum, float inv_k, float eps) { re
 
 // A row per warp (WARP) or per block; vector i * T + t belongs to thread t. What
 // bounds it is memory: 4096 x 4096 bf16 takes 21.5 us, 134 MB at 6.2 TB/s (95% of
-// a copy's rate). Off phase the weights come element by element and three blocks
-// a SM hide that: 1001 x 5127 bf16 11.7 us, with two 13.2; with an fp32 stream
-// and int8 output 16 us, 3.4 TB/s, held by the instructions of the codes.
+// a copy's rate), with an fp32 stream 31.2 us (99%). The int8 rows of a bf16
+// stream, 4096 x 4096 25.8 us for 18.0, are held by instructions (61% of the issue
+// slots); with an fp32 stream 30.2 us for 28.2. Off phase the weights come element
+// by element, which makes the L1 the busiest unit (46%; issue 33%) and the waits
+// for it long; three blocks a SM hide some: 1001 x 5127 bf16 11.6 us, with two
+// 13.2; with an fp32 stream and bf16 output 15.3 us, int8 output 16.3.
 template <int NV, bool WARP, bool ALIGNED, bool HF32, bool WF32>
 __global__ void __launch_bounds__(row_threads(NV, WARP), WARP ? 8 : (NV == 2 ? (ALIGNED ? 2 : 3) : 1))
     rmsnorm_fwd_kernel(const NormArgs a) {
@@ -414,10 +417,13 @@ cudaError_t launch_dw(const float *part, int rows, int64_t K, float *dw, cudaStr
 // columns of all rows. Every block forms all rows' sums for itself (from L2),
 // 32 / M warps a row, so no block waits for another and no partial sums are
 // kept. Where dh or dx overwrites dy, which other blocks would still read, one
-// block does it all. Two launches and a workspace took a call 14 us from the
-// host, this 8 (on the device 8 x 4096 takes 3.9 and 5.4 us). A row's sums come in the persistent kernel's order (vectors
-// warp by warp of its T threads, NV each, then the warps), so that a row's
-// gradient is the same bits whatever stands beside it.
+// block does it all. What it saves is the host's share: a call among others takes
+// 8.6 us (two launches and a workspace 13.7), on the device alone 5.3 us for 8 x
+// 4096 (3.8), 4.3 for 16 x 1024 (3.0), 4.9 for 4 x 8192 (5.2). A call waited for
+// takes 19.9 us for 8 x 4096 (21.8), but 22.6 for 16 x 4096 (21.6) and 25.2 for
+// 16 x 8192 (23.4): hence 32768 elements. A row's sums come in the persistent
+// kernel's order (vectors warp by warp of its T threads, NV each, then the warps),
+// so that a row's gradient is the same bits whatever stands beside it.
 constexpr int kFewRows = 16, kFewCols = 128;
 constexpr int64_t kFewElements = 32768, kFewWidth = 8192;
 template <bool ALIGNED, bool HF32, bool WF32>
