@@ -91,16 +91,15 @@ __device__ __forceinline__ void tmem_ld_frag32(uint32_t taddr, uint32_t (&r)[16]
 // token, and of its weight at a feature: a register of an m16n8k16 fragment.
 // Ranks past r, tokens past M and features past F are zero.
 __device__ __forceinline__ uint32_t lora_act_pair(Waited after, const uint16_t *u, int64_t M, int r, int64_t m, int k) {
-  return m < M && k < r ? load_after(after, reinterpret_cast<const uint32_t *>(u + m * r + k)) : 0u;
+  return load_after(after, reinterpret_cast<const uint32_t *>(u + m * r + k), m < M && k < r);
 }
 template <bool kDx>
 __device__ __forceinline__ uint32_t lora_w_pair(Waited after, const uint16_t *w, int64_t F, int r, int64_t f, int k) {
-  if (f >= F || k >= r) return 0u;
   if constexpr (kDx) {   // A [r, F]
     const uint16_t *a = w + static_cast<int64_t>(k) * F + f;
-    return static_cast<uint32_t>(load_after(after, a)) | (static_cast<uint32_t>(load_after(after, a + F)) << 16);
+    return load_after(after, a, a + F, f < F && k < r);
   } else {               // B [F, r]
-    return load_after(after, reinterpret_cast<const uint32_t *>(w + f * r + k));
+    return load_after(after, reinterpret_cast<const uint32_t *>(w + f * r + k), f < F && k < r);
   }
 }
 

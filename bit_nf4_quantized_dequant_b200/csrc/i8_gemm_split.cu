@@ -67,57 +67,71 @@ __device__ __forceinline__ int4 ld_dsmem_int4(uint32_t addr) {
   return v;
 }
 
-// What a thread needs besides the sums to finish a block: the scales of its two
-// tokens and four features, and the adapter's fragments.
-template <bool kDx, int kSteps>
-struct BlockOperands {
+// What a thread needs besides the sums to finish a block: of its two tokens the
+// scales and the adapter's fragments, and the same of its four features.
+template <int kSteps>
+struct RowOperands {
   float sx[2];
-  float2 sw[2];
   uint32_t u[kSteps ? kSteps : 1][4];
-  uint32_t b[kSteps ? kSteps : 1][2][2];
 
-  __device__ __forceinline__ void load(Waited after, const SplitParams &p, int64_t m0, int64_t f0, int lane) {
+  __device__ __forceinline__ void load(Waited after, const SplitParams &p, int64_t m0, int lane) {
     const int g = lane >> 2, q2 = (lane & 3) * 2;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int64_t m = m0 + g + 8 * i, f = f0 + 8 * i + q2;
+      const int64_t m = m0 + g + 8 * i;
       sx[i] = m < p.M ? load_after(after, p.act_scale + m) : 0.f;
+#pragma unroll
+      for (int ks = 0; ks < kSteps; ++ks)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) u[ks][i + 2 * c] = lora_act_pair(after, p.lora_act, p.M, p.r, m, ks * 16 + c * 8 + q2);
+    }
+  }
+};
+template <bool kDx, int kSteps>
+struct ColOperands {
+  float2 sw[2];
+  uint32_t b[kSteps ? kSteps : 1][2][2];
+
+  __device__ __forceinline__ void load(Waited after, const SplitParams &p, int64_t f0, int lane) {
+    const int g = lane >> 2, q2 = (lane & 3) * 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t f = f0 + 8 * i + q2;
       sw[i] = make_float2(1.f, 1.f);
       if (!kDx && f < p.F) sw[i] = load_after(after, reinterpret_cast<const float2 *>(p.w_scale + f));
 #pragma unroll
       for (int ks = 0; ks < kSteps; ++ks)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const int k = ks * 16 + c * 8 + q2;
-          u[ks][i + 2 * c] = lora_act_pair(after, p.lora_act, p.M, p.r, m, k);
-          b[ks][i][c] = lora_w_pair<kDx>(after, p.lora_w, p.F, p.r, f0 + 8 * i + g, k);
-        }
-    }
-  }
-  // s: the block's sums, fragment by fragment
-  __device__ __forceinline__ void finish(const SplitParams &p, int64_t m0, int64_t f0, int lane, const int (&s)[8]) {
-    const int g = lane >> 2, q2 = (lane & 3) * 2;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float y[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        y[e] = static_cast<float>(s[4 * j + e]) * sx[e >> 1];
-        if constexpr (!kDx) y[e] *= (e & 1) ? sw[j].y : sw[j].x;
-      }
-#pragma unroll
-      for (int ks = 0; ks < kSteps; ++ks) mma_16816(y, u[ks], b[ks][j][0], b[ks][j][1]);
-      const int64_t f = f0 + 8 * j + q2;
-      if (f < p.F) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int64_t m = m0 + g + 8 * i;
-          if (m < p.M) *reinterpret_cast<uint32_t *>(p.out + m * p.F + f) = pack_bf16x2(y[2 * i], y[2 * i + 1]);
-        }
-      }
+        for (int c = 0; c < 2; ++c)
+          b[ks][i][c] = lora_w_pair<kDx>(after, p.lora_w, p.F, p.r, f0 + 8 * i + g, ks * 16 + c * 8 + q2);
     }
   }
 };
+// s: the block's sums, fragment by fragment
+template <bool kDx, int kSteps>
+__device__ __forceinline__ void finish_block(const SplitParams &p, int64_t m0, int64_t f0, int lane, const int (&s)[8],
+                                             const RowOperands<kSteps> &row, const ColOperands<kDx, kSteps> &col) {
+  const int g = lane >> 2, q2 = (lane & 3) * 2;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    float y[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      y[e] = static_cast<float>(s[4 * j + e]) * row.sx[e >> 1];
+      if constexpr (!kDx) y[e] *= (e & 1) ? col.sw[j].y : col.sw[j].x;
+    }
+#pragma unroll
+    for (int ks = 0; ks < kSteps; ++ks) mma_16816(y, row.u[ks], col.b[ks][j][0], col.b[ks][j][1]);
+    const int64_t f = f0 + 8 * j + q2;
+    if (f < p.F) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int64_t m = m0 + g + 8 * i;
+        if (m < p.M) *reinterpret_cast<uint32_t *>(p.out + m * p.F + f) = pack_bf16x2(y[2 * i], y[2 * i + 1]);
+      }
+    }
+  }
+}
 
 template <bool kDx, int kSteps>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -223,12 +237,17 @@ __global__ void __launch_bounds__(kThreads, 2)
   // ---- this warp's part of the accumulator: tokens 32 quad .. + 31, features 64 half .. + 63 ----
   const int quad = warp & 3, half = warp >> 2;
   const int tokens = static_cast<int>(p.M - t0 < kTile ? p.M - t0 : kTile);
-  BlockOperands<kDx, kSteps> op;
+  RowOperands<kSteps> row;
   if (split > 1) {
     // blocks (row of blocks rb, column of blocks cb) that hold tokens, dealt out to the cluster's warps
     const int blocks = (tokens + 15) / 16 * 8, step = split * (kThreads / 32);
     int b = warp * split + rank;
-    if (b < blocks) op.load(after, p, t0 + (b >> 3) * 16, f0 + (b & 7) * 16, lane);   // under the main loop
+    ColOperands<kDx, kSteps> col;
+    auto load = [&](int b) {
+      row.load(after, p, t0 + (b >> 3) * 16, lane);
+      col.load(after, p, f0 + (b & 7) * 16, lane);
+    };
+    if (b < blocks) load(b);   // under the main loop
     int4 *part = reinterpret_cast<int4 *>(ring);   // [block][2][lane]
     // the TMEM loads are warp-wide: every lane takes the same way
     if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.status))) {
@@ -262,14 +281,22 @@ __global__ void __launch_bounds__(kThreads, 2)
             s[0] += lo.x; s[1] += lo.y; s[2] += lo.z; s[3] += lo.w;
             s[4] += hi.x; s[5] += hi.y; s[6] += hi.z; s[7] += hi.w;
           }
-        op.finish(p, t0 + (b >> 3) * 16, f0 + (b & 7) * 16, lane, s);
-        if (b + step < blocks) op.load(after, p, t0 + ((b + step) >> 3) * 16, f0 + ((b + step) & 7) * 16, lane);
+        finish_block(p, t0 + (b >> 3) * 16, f0 + (b & 7) * 16, lane, s, row, col);
+        if (b + step < blocks) load(b + step);
       }
     }
     // no CTA leaves while a peer may still read its partial sums
     cluster_sync_all();
   } else {
-    if (quad * 32 < tokens) op.load(after, p, t0 + quad * 32, f0 + half * 64, lane);   // under the main loop
+    // all four blocks' features under the main loop, where they fit the registers: an
+    // ordinary load does not pass the stores of the block before
+    constexpr int kHeld = kSteps <= 1 ? 4 : 1;
+    ColOperands<kDx, kSteps> col[kHeld];
+    if (quad * 32 < tokens) {
+      row.load(after, p, t0 + quad * 32, lane);
+#pragma unroll
+      for (int c = 0; c < kHeld; ++c) col[c].load(after, p, f0 + half * 64 + c * 16, lane);
+    }
     if (__all_sync(0xffffffffu, mbar_wait(done, 0, abort_flag, p.status))) {
       tc_fence_after();
 #pragma unroll 1
@@ -277,6 +304,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int64_t m0 = t0 + quad * 32 + h * 16;
         if (quad * 32 + h * 16 >= tokens) break;
         uint32_t v[32];
+        if (h) row.load(after, p, m0, lane);
         tmem_ld_frag64(tmem + (static_cast<uint32_t>(quad * 32 + h * 16) << 16) + half * 64, v);
         tmem_ld_wait();
 #pragma unroll
@@ -284,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, 2)
           int s[8];
 #pragma unroll
           for (int e = 0; e < 8; ++e) s[e] = static_cast<int>(v[8 * c + e]);
-          if (h || c) op.load(after, p, m0, f0 + half * 64 + c * 16, lane);
-          op.finish(p, m0, f0 + half * 64 + c * 16, lane, s);
+          if (kHeld == 1 && (h || c)) col[0].load(after, p, f0 + half * 64 + c * 16, lane);
+          finish_block(p, m0, f0 + half * 64 + c * 16, lane, s, row, col[kHeld == 1 ? 0 : c]);
         }
       }
       tc_fence_before();

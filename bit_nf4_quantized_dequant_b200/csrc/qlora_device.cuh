@@ -82,14 +82,34 @@ __device__ __forceinline__ Waited grid_dep_wait() {
   asm volatile("griddepcontrol.wait;\n\tmov.u32 %0, 0;" : "=r"(w.order)::"memory");
   return w;
 }
-__device__ __forceinline__ uint16_t load_after(Waited w, const uint16_t *p) {
-  uint16_t v;
-  asm("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p), "r"(w.order));
-  return v;
-}
 __device__ __forceinline__ uint32_t load_after(Waited w, const uint32_t *p) {
   uint32_t v;
   asm("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p), "r"(w.order));
+  return v;
+}
+// The same, or zero where `in` is false, without a branch; and two 16-bit values
+// from different places as one register.
+__device__ __forceinline__ uint32_t load_after(Waited w, const uint16_t *lo, const uint16_t *hi, bool in) {
+  uint32_t v;
+  asm("{\n\t.reg .pred q;\n\t.reg .b16 l, h;\n\t"
+      "setp.ne.u32 q, %4, 0;\n\t"
+      "mov.b16 l, 0;\n\t"
+      "mov.b16 h, 0;\n\t"
+      "@q ld.global.b16 l, [%1];\n\t"
+      "@q ld.global.b16 h, [%2];\n\t"
+      "mov.b32 %0, {l, h};\n\t}"
+      : "=r"(v)
+      : "l"(lo), "l"(hi), "r"(w.order), "r"(static_cast<uint32_t>(in)));
+  return v;
+}
+__device__ __forceinline__ uint32_t load_after(Waited w, const uint32_t *p, bool in) {
+  uint32_t v;
+  asm("{\n\t.reg .pred q;\n\t"
+      "setp.ne.u32 q, %3, 0;\n\t"
+      "mov.u32 %0, 0;\n\t"
+      "@q ld.global.u32 %0, [%1];\n\t}"
+      : "=&r"(v)
+      : "l"(p), "r"(w.order), "r"(static_cast<uint32_t>(in)));
   return v;
 }
 __device__ __forceinline__ uint4 load_after(Waited w, const uint4 *p) {
