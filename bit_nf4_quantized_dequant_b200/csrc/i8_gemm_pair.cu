@@ -461,27 +461,32 @@ cudaError_t launch_i8_pair(const I8GemmArgs &a, cudaStream_t st) {
 // Single tiles of 128 x 128 as long as one wave of CTAs holds them; past that
 // the pairs' 256 x 256 tiles, which need half the operand bytes per output. A
 // little more than one wave of pairs goes back to single tiles, two to a SM.
-// Measured (rank 16): 512 tokens 4096 x 4096 (128 tiles, 32 pair tiles) 12.9 us
-// split, 16.3 pair; 768 tokens (192, 48) 20.2 and 17.4; 200 tokens 11008 x 4096
-// (172, 43) 21.1 and 18.5; 384 tokens (258, 86) 23.0 and 29.5.
+// Measured (rank 16): 512 tokens 4096 x 4096 (128 tiles, 32 pair tiles) 11.0 us
+// split, 11.8 pair; 768 tokens (192, 48) 18.2 and 14.8; 200 tokens 11008 x 4096
+// (172, 43) 19.5 and 15.5; 384 tokens (258, 86) 20.5 and 21.5.
 //
 // Past rank 16 the single tiles' warp MMAs and fragment loads for the adapter cost
-// more than the pairs' tcgen05 term: 0.35 us (gradient: 0.60) for each further 16
-// ranks and block of 16 x 16 that a warp finishes, 8 / split of them. The pairs
-// in turn do a tile's whole contraction in one place, at 0.13 us (0.32) a step
-// where few tiles are at work, the CTAs of a cluster their part at 0.25 us. Rank
-// 32, split and pair: 4096 tokens 432 x 192 (one way, 2 steps) 9.8 and 6.7 us,
-// 300 tokens 4096 x 1024 (one, 8) 8.5 and 7.5, 1024 tokens 1024 x 4096 (two, 32)
-// 10.8 and 10.1, 256 tokens 1024 x 4096 (eight, 32) 8.3 and 9.3, 256 tokens
-// 1024 x 14336 (eight, 112) 10.9 and 19.8; gradient 10.9 and 10.0, 13.1 and 12.2,
-// 18.0 and 21.5, 11.7 and 17.5, 17.9 and 43.6; at rank 64 of 1024 tokens 14.4 and
-// 10.1, gradient 24.1 and 21.6. Up to 128 tokens half of a pair's tile is empty:
-// 100 of 1040 x 2064 at rank 16, 32 and 64 7.1, 7.7 and 8.9 us split, 8.8 pair.
+// more than the pairs' tcgen05 term: about 0.25 us (gradient: 0.38) for each
+// further 16 ranks and block of 16 x 16 that a warp finishes, 8 / ways of them. The
+// pairs start about 0.9 us later and do a tile's whole contraction in one place,
+// at 0.13 us (0.32) a step where few tiles are at work, the CTAs of a cluster their
+// part at 0.25 us. Measured at ranks 24, 32 and 64, split / pair (ways, steps):
+//   tokens x features x contraction     forward                    gradient
+//   4096 x 432 x 192 (1, 2)       7.6/7.1 8.2/6.8 14.6/6.9    9.7/10.2 9.9/10.1 14.6/10.0
+//   300 x 4096 x 1024 (1, 8)      7.5/7.9 7.7/7.6 10.8/7.7    11.2/12.4 11.7/12.2 16.6/12.4
+//   512 x 4096 x 4096 (1, 32)     12.7/12.4 12.8/12.0 16.0/12.2  20.0/21.8 20.4/21.3 25.5/21.8
+//   700 x 1040 x 2064 (2, 17)     9.9/9.8 10.3/9.7 13.2/9.7   15.7/16.9 15.9/16.8 18.9/17.0
+//   1024 x 1024 x 4096 (2, 32)    9.9/10.6 10.2/10.2 13.2/10.1  16.4/21.7 16.8/21.6 20.3/21.7
+//   300 x 1040 x 2064 (4, 17)     7.9/9.6 7.9/9.5 8.8/9.5     11.8/16.3 11.9/16.2 13.1/16.4
+//   256 x 1024 x 14336 (8, 112)   10.7/20.0 10.8/19.8 11.2/19.9  17.0/43.5 17.0/43.3 18.8/43.8
+// Up to 128 tokens half of a pair's tile is empty: 100 x 1040 x 2064 7.3/9.0,
+// 7.3/8.9, 7.9/8.9 and 9.3/14.0, 9.4/14.0, 10.7/14.2; one way and past rank 32 the
+// pairs would be the faster ones there too (120 x 14336 x 4096 20.4/19.1, 25.3/22.2).
 bool adapter_fits_split(const I8GemmArgs &a) {
   if (a.r <= 16 || a.M <= 128) return true;
   const int64_t nk = (a.C + kI8Step - 1) / kI8Step, ways = i8_split_ways(a.M, a.F, a.C);
-  const int64_t adapter = (a.dx ? 60 : 35) * ((8 + ways - 1) / ways) * ((a.r + 15) / 16 - 1);   // in 10 ns
-  return adapter <= (a.dx ? 32 : 13) * nk - 25 * ((nk + ways - 1) / ways);
+  const int64_t adapter = (a.dx ? 38 : 25) * ((8 + ways - 1) / ways) * ((a.r + 15) / 16 - 1);   // in 10 ns
+  return adapter <= 90 + (a.dx ? 32 : 13) * nk - 25 * ((nk + ways - 1) / ways);
 }
 
 cudaError_t launch_i8_gemm(const I8GemmArgs &a, cudaStream_t st) {

@@ -15,12 +15,12 @@
 // a cluster share the blocks that hold tokens, and each finishes its own:
 // sum, scales, adapter (mma.m16n8k16), bf16, 32-byte row segments stored.
 //
-// Measured: one token of 14336 x 4096 12.1 us, 59 MB at 4.8 TB/s (0.30 us, 6.0
+// Measured: one token of 14336 x 4096 12.0 us, 59 MB at 4.9 TB/s (0.30 us, 6.1
 // TB/s, for each further step of the contraction; the rest is the launch, the
-// filling of a pipeline and the epilogue); of 4096 x 4096 5.2 us, most of it those;
-// 512 tokens of 4096 x 4096 12 us at rank 16. 301 tokens of 1040 x 2064, gradient,
-// rank 8 (51 tiles of 9 steps): 11.7 us in all with 1 or 2 ways, 12.4 with 4, of
-// which quantising is 3.1; one step instead of nine takes 6.3.
+// filling of a pipeline and the epilogue); of 4096 x 4096 5.3 us, most of it those;
+// 512 tokens of 4096 x 4096 11 us at rank 16. 301 tokens of 1040 x 2064, gradient,
+// rank 8 (51 tiles of 9 steps): 11.4 us in all, of which quantising is 3.1; one
+// step instead of nine takes 5.9.
 //
 // Warps: 0 TMA producer, 1 MMA issuer and TMEM owner; all eight finish.
 #include <atomic>
@@ -371,8 +371,11 @@ static int resident_clusters(int split) {
 }
 
 // As many CTAs as there are SMs, each with about four steps or more. Measured
-// with one token of 4096 x 4096 (32 tiles of 32 steps): 4 ways 6.3 us, 3 ways
-// 6.7, 2 ways 7.2, 8 ways (two CTAs a SM) 7.2; 1024 x 4096: 8 ways 5.1, 4 ways 5.9.
+// with one token of 4096 x 4096 (32 tiles of 32 steps): 4 ways 5.2 us, 3 ways
+// 5.5, 2 ways 5.7, one 7.0, 8 ways (two CTAs a SM) 5.8; 1024 x 4096: 8 ways 4.0, 4
+// ways 4.6; 14336 x 4096 (112 tiles): one 11.9, 2 ways 14.2, 4 ways 17.4. The
+// gradient of 301 tokens 1040 x 2064 takes 11.4 us with its 2 ways, 10.7 with one
+// and 12.4 with 4.
 // A cluster stays inside one GPC, which leaves some SMs out: see resident_clusters.
 int i8_split_ways(int64_t M, int64_t F, int64_t C) {
   const int64_t tiles = ((F + kTile - 1) / kTile) * ((M + kTile - 1) / kTile), nk = (C + kI8Step - 1) / kI8Step;
