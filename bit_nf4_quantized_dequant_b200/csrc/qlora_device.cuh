@@ -82,13 +82,8 @@ __device__ __forceinline__ Waited grid_dep_wait() {
   asm volatile("griddepcontrol.wait;\n\tmov.u32 %0, 0;" : "=r"(w.order)::"memory");
   return w;
 }
-__device__ __forceinline__ uint32_t load_after(Waited w, const uint32_t *p) {
-  uint32_t v;
-  asm("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p), "r"(w.order));
-  return v;
-}
-// The same, or zero where `in` is false, without a branch; and two 16-bit values
-// from different places as one register.
+// One register's worth, or zero where `in` is false, without a branch: two 16-bit
+// values from different places, or 32 bits.
 __device__ __forceinline__ uint32_t load_after(Waited w, const uint16_t *lo, const uint16_t *hi, bool in) {
   uint32_t v;
   asm("{\n\t.reg .pred q;\n\t.reg .b16 l, h;\n\t"

@@ -108,8 +108,8 @@ qlora_status_t qlora_i8_linear_workspace(int64_t M, int64_t N, int64_t K, size_t
 /* The gradient of the 8-bit linear's input, W frozen, through int8 products:
  *   (gq, sg) = qlora_i8_quantize of dY with col_scale = sw (rows of N)
  *   dX[m, k] = bf16_rn(fp32(sum_n gq[m, n] Wq[n, k]) sg[m] + sum_j sT[m, j] A[j, k])
- * An element of dY is off by up to half its row's step, max_n |dY sw| / 254: a row
- * with one loud element loses what is far smaller.
+ * An element of dY sw is off by up to half its row's step, max_n |dY sw| / 254: a
+ * row with one loud element loses what is far smaller.
  * dY [M, N] bf16; sT [M, r] and A [r, K] bf16 as in qlora_fused_dx, or r = 0.
  * dX [M, K] bf16. The adapter's gradients are qlora_lora_grads as for the NF4
  * linear. M >= 1, N % 16 == 0, K % 16 == 0, N <= 65536; K, which is not summed
