@@ -265,3 +265,57 @@ def test_captured_fork_and_join(lib):
         want = lib.i8_linear_fwd(lib.i8_quantize(wide), lib.rmsnorm_fwd(x, w, EPS, q=lib.I8Matrix.empty(M, K))[2])
         assert torch.equal(got, want)
     del graph
+
+
+@pytest.mark.parametrize("M", [1, 8, 16])
+def test_few_token_launches_between_8_bit_products(lib, M):
+    """Few-token NF4 launches that start early (one workspace for all) in a chain
+    with norms and 8-bit products, each reading the one before: eager and replayed,
+    the bits of the same calls with a synchronisation after each."""
+    import torch
+    K, r, s = 512, 16, 2.0
+    g = torch.Generator().manual_seed(M)
+    rn = lambda *sh: torch.randn(*sh, generator=g).cuda()
+    base, W = lib.nf4_quantize(0.04 * rn(K, K)), lib.i8_quantize(0.04 * rn(K, K))
+    A, B, w = (rn(r, K) / r).bfloat16(), (0.01 * rn(K, r)).bfloat16(), 1 + 0.1 * rn(K)
+    x = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    bufs = [torch.empty_like(x) for _ in range(8)]
+    X, Z = lib.I8Matrix.empty(M, K), lib.I8Matrix.empty(M, K)
+    probs = [lib.LinearProblem(base, bufs[i], A, B, s, bufs[i + 1]) for i in (1, 2, 5)]
+    ws = torch.zeros(lib.linear_fwd_group_workspace(probs[:1], M), dtype=torch.uint8, device="cuda")
+
+    def nf4(i):
+        lib.linear_fwd_group([probs[i]], ws=ws, flags=lib.FWD_OVERLAP_PREVIOUS)
+
+    steps = [lambda: lib.rmsnorm_fwd(x, w, EPS, Y=bufs[0], q=X),
+             lambda: lib.i8_linear_fwd(W, X, Y=bufs[1]),
+             lambda: nf4(0),
+             lambda: nf4(1),
+             lambda: lib.rmsnorm_fwd(bufs[3], w, EPS, residual=bufs[0], H=bufs[4], q=Z),
+             lambda: lib.i8_linear_fwd(W, Z, Y=bufs[5]),
+             lambda: nf4(2),
+             lambda: lib.i8_linear_dx(W, bufs[6], dX=bufs[7])]
+
+    def chain(after=False):
+        for step in steps:
+            step()
+            if after:
+                torch.cuda.synchronize()
+
+    chain(after=True)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        chain()
+    for _ in range(20):
+        x.copy_(rn(M, K))
+        torch.cuda.synchronize()
+        chain(after=True)
+        want = [b.clone() for b in bufs]
+        for run in (chain, graph.replay):
+            for b in bufs:
+                b.fill_(7)
+            for _ in range(3):
+                run()
+            for a, b in zip(want, bufs):
+                assert torch.equal(a, b)
+    del graph
